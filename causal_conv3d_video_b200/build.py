@@ -2,8 +2,9 @@
 
     python -m causal_conv3d_video_b200.build [--force] [--verbose-ptxas]
 
-The library is a single translation unit (csrc/ccv3d.cu) exporting the C ABI
-declared in include/ccv3d.h.  The CUDA runtime is linked statically; the
+The library is two translation units (csrc/ccv3d.cu: the convolution,
+csrc/ccv3d_block.cu: the operators around it) exporting the C ABI declared in
+include/ccv3d.h.  The CUDA runtime is linked statically; the
 driver's cuTensorMapEncodeTiled is reached through cudaGetDriverEntryPoint,
 so no -lcuda is needed at link time.
 """
@@ -55,7 +56,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, checked: bool = Fals
     cmd = [_nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared",
            "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
            "-I", os.path.join(ROOT, "include"),
-           os.path.join(CSRC, "ccv3d.cu"), "-o", tmp]
+           "--threads", "2", os.path.join(CSRC, "ccv3d.cu"),
+           os.path.join(CSRC, "ccv3d_block.cu"), "-o", tmp]
     if checked:
         cmd[1:1] = ["-DCCV3D_CHECKED"]
     if verbose_ptxas:

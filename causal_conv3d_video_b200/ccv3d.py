@@ -31,7 +31,10 @@ EXPORTED = ("ccv3d_plan", "ccv3d_plan_intervals", "ccv3d_plan_path", "ccv3d_forw
             "ccv3d_plan_sizes", "ccv3d_selftest_wait_timeout", "ccv3d_forward_noalloc",
             "ccv3d_plan_kernel", "ccv3d_plan_tiling", "ccv3d_quantize_u8",
             "ccv3d_get_status_stream", "ccv3d_noalloc_get_status", "ccv3d_forward_ring",
-            "ccv3d_selftest_bounds")
+            "ccv3d_selftest_bounds", "ccv3d_norm_forward", "ccv3d_norm_workspace",
+            "ccv3d_norm_backward", "ccv3d_pointwise_workspace", "ccv3d_pointwise_forward",
+            "ccv3d_pointwise_backward", "ccv3d_qcache_sizes", "ccv3d_qcache_write",
+            "ccv3d_qcache_read", "ccv3d_forward_qring", "ccv3d_block_get_status")
 CCV3D_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 
@@ -46,6 +49,27 @@ class ccv3d_stats(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in (
         "calls", "tc_path", "simt_path", "unsupported", "errors", "workspace_bytes",
         "plans_unsupported")]
+
+
+NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
+ACTS = {"none": 0, "silu": 1, "gelu": 2}
+QFORMATS = {"int8": 0, "e4m3": 1, "e2m1": 2}
+
+
+class ccv3d_norm_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("C", ctypes.c_int), ("pre", ctypes.c_int),
+                ("post", ctypes.c_int), ("act", ctypes.c_int), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("gate_rows", ctypes.c_longlong),
+                ("dtype", ctypes.c_int)]
+
+
+class ccv3d_pointwise_desc(ctypes.Structure):
+    _fields_ = [("pixels", ctypes.c_longlong), ("Cin", ctypes.c_int), ("Cout", ctypes.c_int),
+                ("act", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class ccv3d_qcache_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("N", "C", "H", "W", "ring_slots", "format", "dtype")]
 
 
 class CCV3DError(RuntimeError):
@@ -89,6 +113,27 @@ def _load():
     lib.ccv3d_noalloc_get_status.argtypes = [vp]
     lib.ccv3d_forward_ring.argtypes = [vp, vp, vp, ctypes.c_int, ctypes.c_int, vp, vp, vp,
                                        ip, ip, ip, vp, ip]
+    c_int, c_size, p_size = ctypes.c_int, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+    norm, point, qcache = (ctypes.POINTER(t) for t in (ccv3d_norm_desc, ccv3d_pointwise_desc,
+                                                       ccv3d_qcache_desc))
+    lib.ccv3d_norm_forward.argtypes = [norm] + [vp] * 10
+    lib.ccv3d_norm_workspace.argtypes = [norm]
+    lib.ccv3d_norm_workspace.restype = c_size
+    lib.ccv3d_norm_backward.argtypes = [norm] + [vp] * 17 + [c_size, vp]
+    lib.ccv3d_pointwise_workspace.argtypes = [point, p_size, p_size]
+    lib.ccv3d_pointwise_forward.argtypes = [point] + [vp] * 7 + [c_size, vp]
+    lib.ccv3d_pointwise_backward.argtypes = [point] + [vp] * 8 + [c_size, vp]
+    lib.ccv3d_qcache_sizes.argtypes = [qcache, p_size, p_size]
+    lib.ccv3d_qcache_write.argtypes = [qcache, vp, c_int, c_int, c_int, c_int, vp, vp, vp]
+    lib.ccv3d_qcache_read.argtypes = [qcache, vp, vp, c_int, c_int, vp, vp]
+    lib.ccv3d_forward_qring.argtypes = [vp, vp, qcache, vp, vp, c_int, vp, vp, vp, vp, ip, ip, ip,
+                                        vp, ip]
+    lib.ccv3d_block_get_status.argtypes = [vp]
+    for f in ("ccv3d_norm_forward", "ccv3d_norm_backward", "ccv3d_pointwise_workspace",
+              "ccv3d_pointwise_forward", "ccv3d_pointwise_backward", "ccv3d_qcache_sizes",
+              "ccv3d_qcache_write", "ccv3d_qcache_read", "ccv3d_forward_qring",
+              "ccv3d_block_get_status"):
+        getattr(lib, f).restype = c_int
     for f in ("ccv3d_plan", "ccv3d_plan_intervals", "ccv3d_forward", "ccv3d_get_stats",
               "ccv3d_get_status", "ccv3d_plan_sizes", "ccv3d_selftest_wait_timeout",
               "ccv3d_forward_noalloc", "ccv3d_get_status_stream", "ccv3d_noalloc_get_status",
@@ -267,7 +312,216 @@ def ccv3d_selftest_bounds(stream=None) -> int:
     return lib.ccv3d_selftest_bounds(_stream(stream))
 
 
+# ------------------------------------------- the operators around the convolution
+_TORCH_DTYPES = None
+
+
+def _operands(where, dtype, pairs):
+    """Device addresses of a call's buffers.  pairs: (name, tensor or address
+    or None, elements or None, torch dtype name or None for the call's).
+    Tensors must be contiguous, of the element type and size the call reads or
+    writes, on the current CUDA device; raises ValueError otherwise.  Raw
+    addresses are the caller's word."""
+    import torch
+    global _TORCH_DTYPES
+    if _TORCH_DTYPES is None:
+        _TORCH_DTYPES = {CCV3D_BF16: torch.bfloat16, CCV3D_FP32: torch.float32,
+                         "uint8": torch.uint8}
+    out, device = [], None
+    for name, t, n, dt in pairs:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        want = _TORCH_DTYPES.get(dtype if dt is None else dt)
+        if want is not None and t.dtype != want:
+            raise ValueError(f"{where}: {name} is {t.dtype}, not {want}")
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{where}: {name} has {t.numel()} elements, not {n}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} is not contiguous")
+        if device is None:
+            device = torch.cuda.current_device() if t.is_cuda else -1
+        if not t.is_cuda or t.get_device() != device:
+            raise ValueError(f"{where}: {name} is on {t.device}, not on the current CUDA device")
+        out.append(t.data_ptr())
+    return out
+
+
+def _status(rc, where, check):
+    if rc != 0 and check:
+        raise CCV3DError(rc, where)
+    return rc
+
+
+def _ws(where, ws):
+    """Address and bytes of a workspace: a tensor (any type, contiguous) or None."""
+    if ws is None:
+        return None, 0
+    return _operands(where, "any", [("ws", ws, None, "any")])[0], ws.numel() * ws.element_size()
+
+
+def ccv3d_norm_workspace(desc: ccv3d_norm_desc) -> int:
+    return lib.ccv3d_norm_workspace(ctypes.byref(desc))
+
+
+def ccv3d_norm_forward(desc: ccv3d_norm_desc, h, b, gate, post_w, post_bias, pre_w, pre_bias,
+                       h_out, y, stream=None, check: bool = True) -> int:
+    """h_out = h + scale * gate * post(b); y = act(pre(h_out)).  Tensors as the
+    C call's comment lists them (None for NULL).  Raises CCV3DError on a
+    refused call unless check=False."""
+    n, C = desc.rows * desc.C, desc.C
+    gates = n // desc.gate_rows if gate is not None and desc.gate_rows > 0 else None
+    a = _operands("ccv3d_norm_forward", desc.dtype, (
+        ("h", h, n, None), ("b", b, n, None), ("gate", gate, gates, None),
+        ("post_w", post_w, C, None), ("post_bias", post_bias, C, None), ("pre_w", pre_w, C, None),
+        ("pre_bias", pre_bias, C, None), ("h_out", h_out, n, None), ("y", y, n, None)))
+    return _status(lib.ccv3d_norm_forward(ctypes.byref(desc), *a, _stream(stream)),
+                   "ccv3d_norm_forward", check)
+
+
+def ccv3d_norm_backward(desc: ccv3d_norm_desc, h_out, b, gate, post_w, post_bias, pre_w, pre_bias,
+                        dy, dh_out, dh, db, dgate, dpost_w, dpost_bias, dpre_w, dpre_bias, ws,
+                        stream=None, check: bool = True) -> int:
+    """Gradients of ccv3d_norm_forward (None for those not wanted); ws: a
+    workspace of at least ccv3d_norm_workspace(desc) bytes."""
+    n, C = desc.rows * desc.C, desc.C
+    gates = n // desc.gate_rows if gate is not None and desc.gate_rows > 0 else None
+    where = "ccv3d_norm_backward"
+    a = _operands(where, desc.dtype, (
+        ("h_out", h_out, n, None), ("b", b, n, None), ("gate", gate, gates, None),
+        ("post_w", post_w, C, None), ("post_bias", post_bias, C, None), ("pre_w", pre_w, C, None),
+        ("pre_bias", pre_bias, C, None), ("dy", dy, n, None), ("dh_out", dh_out, n, None),
+        ("dh", dh, n, None), ("db", db, n, None), ("dgate", dgate, gates, None),
+        ("dpost_w", dpost_w, C, None), ("dpost_bias", dpost_bias, C, None),
+        ("dpre_w", dpre_w, C, None), ("dpre_bias", dpre_bias, C, None)))
+    return _status(lib.ccv3d_norm_backward(ctypes.byref(desc), *a, *_ws(where, ws),
+                                           _stream(stream)), where, check)
+
+
+def ccv3d_pointwise_workspace(desc: ccv3d_pointwise_desc):
+    """(forward, backward) workspace bytes."""
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _status(lib.ccv3d_pointwise_workspace(ctypes.byref(desc), ctypes.byref(f), ctypes.byref(b)),
+            "ccv3d_pointwise_workspace", True)
+    return f.value, b.value
+
+
+def ccv3d_pointwise_forward(desc: ccv3d_pointwise_desc, x, w, bias, residual, out, pre, ws,
+                            stream=None, check: bool = True) -> int:
+    """out = act(x w^T + bias) + residual; pre (None: not wanted) receives the
+    argument of act."""
+    M, K, N = desc.pixels, desc.Cin, desc.Cout
+    where = "ccv3d_pointwise_forward"
+    a = _operands(where, desc.dtype, (
+        ("x", x, M * K, None), ("w", w, N * K, None), ("bias", bias, N, None),
+        ("residual", residual, M * N, None), ("out", out, M * N, None), ("pre", pre, M * N, None)))
+    return _status(lib.ccv3d_pointwise_forward(ctypes.byref(desc), *a, *_ws(where, ws),
+                                               _stream(stream)), where, check)
+
+
+def ccv3d_pointwise_backward(desc: ccv3d_pointwise_desc, x, w, pre, dout, dx, dw, dbias, ws,
+                             stream=None, check: bool = True) -> int:
+    """Gradients of ccv3d_pointwise_forward (None for those not wanted)."""
+    M, K, N = desc.pixels, desc.Cin, desc.Cout
+    where = "ccv3d_pointwise_backward"
+    a = _operands(where, desc.dtype, (
+        ("x", x, M * K, None), ("w", w, N * K, None), ("pre", pre, M * N, None),
+        ("dout", dout, M * N, None), ("dx", dx, M * K, None), ("dw", dw, N * K, None),
+        ("dbias", dbias, N, None)))
+    return _status(lib.ccv3d_pointwise_backward(ctypes.byref(desc), *a, *_ws(where, ws),
+                                                _stream(stream)), where, check)
+
+
+def ccv3d_qcache_sizes(desc: ccv3d_qcache_desc):
+    """(codes, scales) bytes."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _status(lib.ccv3d_qcache_sizes(ctypes.byref(desc), ctypes.byref(c), ctypes.byref(s)),
+            "ccv3d_qcache_sizes", True)
+    return c.value, s.value
+
+
+def _ring_bytes(desc):
+    px = desc.N * desc.ring_slots * desc.H * desc.W
+    return (px * ((desc.C + 1) // 2 if desc.format == QFORMATS["e2m1"] else desc.C),
+            px * ((desc.C + 31) // 32))
+
+
+def ccv3d_qcache_write(desc: ccv3d_qcache_desc, x, T_x: int, first: int, frames: int, slot: int,
+                       codes, scales, stream=None, check: bool = True) -> int:
+    """Quantise frames [first, first + frames) of x into ring slots from `slot` on."""
+    cb, sb = _ring_bytes(desc)
+    a = _operands("ccv3d_qcache_write", desc.dtype, (
+        ("x", x, desc.N * T_x * desc.H * desc.W * desc.C, None), ("codes", codes, cb, "uint8"),
+        ("scales", scales, sb, "uint8")))
+    return _status(lib.ccv3d_qcache_write(ctypes.byref(desc), a[0], T_x, first, frames, slot, a[1],
+                                          a[2], _stream(stream)), "ccv3d_qcache_write", check)
+
+
+def ccv3d_qcache_read(desc: ccv3d_qcache_desc, codes, scales, head: int, frames: int, out,
+                      stream=None, check: bool = True) -> int:
+    """Read ring slots from `head` on back into `frames` dense frames."""
+    cb, sb = _ring_bytes(desc)
+    a = _operands("ccv3d_qcache_read", desc.dtype, (
+        ("codes", codes, cb, "uint8"), ("scales", scales, sb, "uint8"),
+        ("out", out, desc.N * frames * desc.H * desc.W * desc.C, None)))
+    return _status(lib.ccv3d_qcache_read(ctypes.byref(desc), a[0], a[1], head, frames, a[2],
+                                         _stream(stream)), "ccv3d_qcache_read", check)
+
+
+def ccv3d_forward_qring(plan, x, desc: ccv3d_qcache_desc, codes, scales, head: int, cache_buf, w,
+                        bias, out, stride, pad, dilation, stream=None, check: bool = True):
+    """ccv3d_forward_ring with the ring held in 8 or 4 bits.  Returns (status,
+    next_head)."""
+    cb, sb = _ring_bytes(desc)
+    dt = desc.dtype
+    a = _operands("ccv3d_forward_qring", dt, (
+        ("x", x, None, None), ("codes", codes, cb, "uint8"), ("scales", scales, sb, "uint8"),
+        ("cache_buf", cache_buf, None, None), ("w", w, None, None), ("bias", bias, None, None),
+        ("out", out, None, None)))
+    s, p, d = (ctypes.c_int * 2)(*stride), (ctypes.c_int * 2)(*pad), (ctypes.c_int * 3)(*dilation)
+    nh = ctypes.c_int(-1)
+    rc = lib.ccv3d_forward_qring(plan, a[0], ctypes.byref(desc), a[1], a[2], int(head), a[3], a[4],
+                                 a[5], a[6], s, p, d, _stream(stream), ctypes.byref(nh))
+    return _status(rc, "ccv3d_forward_qring", check), nh.value
+
+
+def ccv3d_block_get_status(stream=None) -> int:
+    return lib.ccv3d_block_get_status(_stream(stream))
+
+
 # ---------------------------------------------------------------- helpers
+def _dtype_code(dtype):
+    return {"bf16": CCV3D_BF16, "fp32": CCV3D_FP32}[dtype]
+
+
+def make_norm_desc(*, rows, C, pre="rms", post="none", act="none", eps=1e-6, scale=1.0,
+                   gate_rows=0, dtype="bf16") -> ccv3d_norm_desc:
+    """gate_rows: consecutive rows that share a row of the gate (0: no gate)."""
+    return ccv3d_norm_desc(rows, C, NORM_KINDS[pre], NORM_KINDS[post], ACTS[act], eps, scale,
+                           gate_rows, _dtype_code(dtype))
+
+
+def make_pointwise_desc(*, pixels, Cin, Cout, act="none", dtype="bf16") -> ccv3d_pointwise_desc:
+    return ccv3d_pointwise_desc(pixels, Cin, Cout, ACTS[act], _dtype_code(dtype))
+
+
+def make_qcache_desc(*, N, H, W, C, ring_slots, format="int8", dtype="bf16") -> ccv3d_qcache_desc:
+    return ccv3d_qcache_desc(N, C, H, W, ring_slots, QFORMATS[format], _dtype_code(dtype))
+
+
+def alloc_workspace(nbytes: int, device="cuda"):
+    """A workspace of that many bytes (None for 0)."""
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def alloc_qcache(desc: ccv3d_qcache_desc, device="cuda"):
+    """(codes, scales) of a quantised ring cache, empty."""
+    import torch
+    return tuple(torch.zeros(n, dtype=torch.uint8, device=device)
+                 for n in ccv3d_qcache_sizes(desc))
+
+
 def make_desc(*, N, Cin, Cout, H, W, T_x, cache_len, kt=3, kh=3, kw=3,
               pad_t_base=None, cache_keep=None, stride=(1, 1), pad=(1, 1),
               dilation=(1, 1, 1), dtype="bf16", has_bias=True, stride_t=1,
@@ -331,6 +585,11 @@ class Plan:
         """Ring-buffer cache call; returns the head of the new cache."""
         return ccv3d_forward_ring(self.handle, x, ring, ring_slots, head, w, bias, out,
                                   self.stride, self.pad, self.dilation, stream)[1]
+
+    def forward_qring(self, x, desc, codes, scales, head, cache_buf, w, bias, out, stream=None):
+        """Call with its ring cache in 8 or 4 bits; returns the head of the new cache."""
+        return ccv3d_forward_qring(self.handle, x, desc, codes, scales, head, cache_buf, w, bias,
+                                   out, self.stride, self.pad, self.dilation, stream)[1]
 
     def ring_writes(self):
         """Frames of x a ring-buffer call writes into the ring."""

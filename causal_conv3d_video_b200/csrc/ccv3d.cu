@@ -1196,10 +1196,11 @@ ccv3d_status run_simt(ccv3d_plan_s* p, const void* x, const CacheIO& io, const v
     return cudaGetLastError() == cudaSuccess ? CCV3D_OK : CCV3D_ERR_CUDA;
 }
 
-// Argument checks of a forward call against its plan (no device work).
+// Argument checks of a forward call against its plan (no device work); keep:
+// the frames that the call writes to new_cache.
 ccv3d_status check_call(const ccv3d_plan_s* p, const void* x, const void* cache, const void* w,
                         const void* bias, const void* out, const void* nc, const int stride[2],
-                        const int pad[2], const int dilation[3]) {
+                        const int pad[2], const int dilation[3], int keep) {
     const ccv3d_desc& d = p->d;
     if (stride == nullptr || pad == nullptr || dilation == nullptr) return CCV3D_ERR_INVALID;
     if (stride[0] != d.stride_h || stride[1] != d.stride_w || pad[0] != d.pad_h ||
@@ -1207,7 +1208,7 @@ ccv3d_status check_call(const ccv3d_plan_s* p, const void* x, const void* cache,
         dilation[2] != d.dil_w)
         return CCV3D_ERR_INVALID;
     if (x == nullptr || w == nullptr || out == nullptr || (d.cache_len > 0 && cache == nullptr) ||
-        (d.has_bias && bias == nullptr) || (p->keep > 0 && nc == nullptr))
+        (d.has_bias && bias == nullptr) || (keep > 0 && nc == nullptr))
         return CCV3D_ERR_INVALID;
     if (!aligned16(x) || !aligned16(w) || !aligned16(out) ||
         (d.cache_len > 0 && !aligned16(cache)) || (nc != nullptr && !aligned16(nc)) ||
@@ -1217,7 +1218,7 @@ ccv3d_status check_call(const ccv3d_plan_s* p, const void* x, const void* cache,
     const size_t frame = (size_t)d.H * d.W * d.Cin * e;
     const size_t x_bytes = (size_t)d.N * d.T_x * frame;
     const size_t c_bytes = d.cache_len > 0 ? (size_t)d.N * d.cache_len * frame : 0;
-    const size_t nc_bytes = nc != nullptr ? (size_t)d.N * p->keep * frame : 0;
+    const size_t nc_bytes = nc != nullptr ? (size_t)d.N * keep * frame : 0;
     const size_t o_bytes = (size_t)d.N * p->T_o * p->H_o * p->W_o * d.Cout * e;
     const size_t w_bytes = (size_t)d.Cout * d.kt * d.kh * d.kw * d.Cin * e;
     if (overlaps(nc, nc_bytes, x, x_bytes) || overlaps(nc, nc_bytes, cache, c_bytes) ||
@@ -1418,7 +1419,7 @@ ccv3d_status ccv3d_forward(ccv3d_plan_t p, const void* x, const void* cache, con
             .fetch_add(1, std::memory_order_relaxed);
         return s;
     };
-    const ccv3d_status chk = check_call(p, x, cache, w, bias, out, nc, stride, pad, dilation);
+    const ccv3d_status chk = check_call(p, x, cache, w, bias, out, nc, stride, pad, dilation, p->keep);
     if (chk != CCV3D_OK) return refuse(chk);
     if (p->d_status == nullptr) return refuse(CCV3D_ERR_CUDA);
     int dev = -1;
@@ -1464,6 +1465,82 @@ ccv3d_status ccv3d_forward_ring(ccv3d_plan_t p, const void* x, void* ring, int r
     if (next_head != nullptr)
         *next_head = (int)(((long long)head + d.cache_len + writes - p->keep) % ring_slots +
                            ring_slots) % ring_slots;
+    p->calls.fetch_add(1, std::memory_order_relaxed);
+    (p->path_tc ? p->tc : p->simt).fetch_add(1, std::memory_order_relaxed);
+    return CCV3D_OK;
+}
+
+// The quantised ring: read back into the caller's scratch, convolve, quantise
+// what arrived.  Everything is checked before the first launch, so a refused
+// call changes neither the ring nor the scratch.
+ccv3d_status ccv3d_forward_qring(ccv3d_plan_t p, const void* x, const ccv3d_qcache_desc* q,
+                                 void* codes, void* scales, int head, void* cache_buf,
+                                 const void* w, const void* bias, void* out, const int stride[2],
+                                 const int pad[2], const int dilation[3], cudaStream_t stream,
+                                 int* next_head) {
+    if (p == nullptr) return CCV3D_ERR_INVALID;
+    auto refuse = [&](ccv3d_status s) {
+        (s == CCV3D_ERR_UNSUPPORTED ? p->unsupported : p->errors)
+            .fetch_add(1, std::memory_order_relaxed);
+        return s;
+    };
+    const ccv3d_desc& d = p->d;
+    size_t cb = 0, sb = 0;
+    ccv3d_status st = ccv3d_qcache_sizes(q, &cb, &sb);
+    if (st != CCV3D_OK) return refuse(st);
+    const int writes = ring_writes(p), slots = q->ring_slots;
+    const bool uses_ring = d.cache_len > 0 || writes > 0;
+    if (q->N != d.N || q->C != d.Cin || q->H != d.H || q->W != d.W || q->dtype != d.dtype ||
+        head < 0 || head >= slots || d.cache_len + writes > slots ||
+        (uses_ring && (codes == nullptr || scales == nullptr)))
+        return refuse(CCV3D_ERR_INVALID);
+    // the plain forward call's checks, with no new_cache of its own
+    const int keep = p->keep;
+    st = check_call(p, x, cache_buf, w, bias, out, nullptr, stride, pad, dilation, 0);
+    if (st != CCV3D_OK) return refuse(st);
+    const size_t frame = (size_t)d.H * d.W * d.Cin * elt(d);
+    const size_t x_bytes = (size_t)d.N * d.T_x * frame;
+    const size_t c_bytes = (size_t)d.N * d.cache_len * frame;
+    const size_t o_bytes = (size_t)d.N * p->T_o * p->H_o * p->W_o * d.Cout * elt(d);
+    const size_t w_bytes = (size_t)d.Cout * d.kt * d.kh * d.kw * d.Cin * elt(d);
+    const size_t b_bytes = d.has_bias ? (size_t)d.Cout * elt(d) : 0;
+    if (uses_ring) {
+        if (!aligned16(codes) || !aligned16(scales)) return refuse(CCV3D_ERR_ALIGNMENT);
+        const void* at[2] = {codes, scales};
+        const size_t bytes[2] = {cb, sb};
+        bool alias = overlaps(codes, cb, scales, sb);
+        for (int i = 0; i < 2; ++i)
+            alias = alias || overlaps(at[i], bytes[i], x, x_bytes) ||
+                    overlaps(at[i], bytes[i], cache_buf, c_bytes) ||
+                    overlaps(at[i], bytes[i], out, o_bytes) ||
+                    overlaps(at[i], bytes[i], w, w_bytes) ||
+                    overlaps(at[i], bytes[i], bias, b_bytes);
+        if (alias) return refuse(CCV3D_ERR_ALIAS);
+    }
+    if (overlaps(cache_buf, c_bytes, x, x_bytes) || overlaps(cache_buf, c_bytes, w, w_bytes) ||
+        overlaps(cache_buf, c_bytes, bias, b_bytes))
+        return refuse(CCV3D_ERR_ALIAS);
+    if ((long long)d.N * std::max(d.cache_len, writes) > 65535)
+        return refuse(CCV3D_ERR_UNSUPPORTED);
+    if (p->d_status == nullptr) return refuse(CCV3D_ERR_CUDA);
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != p->device) return refuse(CCV3D_ERR_INVALID);
+    if (d.cache_len > 0) {
+        st = ccv3d_qcache_read(q, codes, scales, head, d.cache_len, cache_buf, stream);
+        if (st != CCV3D_OK) return refuse(st);
+    }
+    const CacheIO io = dense_io(p, cache_buf, nullptr);
+    st = p->path_tc ? run_tc(p, x, io, w, bias, out, stream)
+                    : run_simt(p, x, io, w, bias, out, stream);
+    if (st != CCV3D_OK) return refuse(st);
+    if (writes > 0) {
+        st = ccv3d_qcache_write(q, x, d.T_x, d.T_x - writes, writes,
+                                (int)(((long long)head + d.cache_len) % slots), codes, scales,
+                                stream);
+        if (st != CCV3D_OK) return refuse(st);
+    }
+    if (next_head != nullptr)
+        *next_head = (int)((((long long)head + d.cache_len + writes - keep) % slots + slots) % slots);
     p->calls.fetch_add(1, std::memory_order_relaxed);
     (p->path_tc ? p->tc : p->simt).fetch_add(1, std::memory_order_relaxed);
     return CCV3D_OK;
@@ -1516,7 +1593,8 @@ const char* ccv3d_strerror(ccv3d_status s) {
         case CCV3D_ERR_CUDA: return "CUDA error";
         case CCV3D_ERR_TIMEOUT: return "bounded device wait timed out";
         case CCV3D_ERR_SCRATCH_LIMIT:
-            return "call needs more device scratch than the no-allocation entry point holds";
+            return "call needs more device scratch than the no-allocation entry point's array or "
+                   "the given workspace holds";
         case CCV3D_ERR_BOUNDS:
             return "bounds-checked build: a kernel computed an address outside its buffer";
     }
@@ -1625,7 +1703,7 @@ extern "C" ccv3d_status ccv3d_forward_noalloc(const ccv3d_desc* desc, const void
     choose_path(*desc, &p);
     if (!p.path_tc || !setup_persistent(*desc, &p)) return CCV3D_ERR_UNSUPPORTED;
     size_tc(*desc, &p);
-    st = check_call(&p, x, cache, w, bias, out, nc, stride, pad, dilation);
+    st = check_call(&p, x, cache, w, bias, out, nc, stride, pad, dilation, p.keep);
     if (st != CCV3D_OK) return st;
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) {

@@ -1,0 +1,658 @@
+// ccv3d_block.cu -- C ABI of the operators around the convolution: block norms
+// (ccv3d_norm_*), the 1x1x1 product (ccv3d_pointwise_*) and the quantised ring
+// cache (ccv3d_qcache_*).  Argument checks, launch shapes and launches; the
+// kernels and the mathematics are in the headers.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "ccv3d.h"
+#include "elem.cuh"
+#include "norm.cuh"
+#include "pointwise_simt.cuh"
+#include "qcache.cuh"
+
+using namespace ccv3d;
+
+namespace {
+
+constexpr int kSms = 148;  // B200
+typedef __nv_bfloat16 bf16;
+
+ccv3d_status launched() { return cudaGetLastError() == cudaSuccess ? CCV3D_OK : CCV3D_ERR_CUDA; }
+bool known(ccv3d_dtype t) { return t == CCV3D_BF16 || t == CCV3D_FP32; }
+size_t size_of(ccv3d_dtype t) { return t == CCV3D_BF16 ? 2 : 4; }
+long long up(long long a, long long b) { return (a + b - 1) / b; }
+
+// The buffers of a call: every one 16-byte aligned, no written one
+// overlapping another.  NULL and empty buffers are left out.
+struct Buffers {
+    struct One { uintptr_t at; size_t bytes; bool written; };
+    One b[24];
+    int n = 0;
+    bool aligned = true, alias = false;
+    void add(const void* p, size_t bytes, bool written) {
+        if (p == nullptr || bytes == 0) return;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        if (a & 15u) aligned = false;
+        for (int i = 0; i < n; ++i)
+            if ((written || b[i].written) && a < b[i].at + b[i].bytes && b[i].at < a + bytes)
+                alias = true;
+        b[n++] = {a, bytes, written};
+    }
+    void in(const void* p, size_t bytes) { add(p, bytes, false); }
+    void out(const void* p, size_t bytes) { add(p, bytes, true); }
+    ccv3d_status check() const {
+        return !aligned ? CCV3D_ERR_ALIGNMENT : (alias ? CCV3D_ERR_ALIAS : CCV3D_OK);
+    }
+};
+
+// ------------------------------------------------------------------- norms
+ccv3d_status check_norm(const ccv3d_norm_desc* d) {
+    if (d == nullptr) return CCV3D_ERR_INVALID;
+    if (!known(d->dtype) || d->pre < CCV3D_NORM_NONE || d->pre > CCV3D_NORM_LAYER ||
+        d->post < CCV3D_NORM_NONE || d->post > CCV3D_NORM_LAYER || d->act < CCV3D_ACT_NONE ||
+        d->act > CCV3D_ACT_GELU)
+        return CCV3D_ERR_UNSUPPORTED;
+    if (d->rows < 0 || d->C < 1 || !(d->eps > 0.0f) || !std::isfinite(d->eps) ||
+        !std::isfinite(d->scale))
+        return CCV3D_ERR_INVALID;
+    if (d->C > CCV3D_NORM_MAX_C || d->rows > (1LL << 46) / d->C) return CCV3D_ERR_UNSUPPORTED;
+    return CCV3D_OK;
+}
+
+bool gate_fits(const ccv3d_norm_desc* d, const void* gate) {
+    return gate == nullptr || (d->gate_rows >= 1 && d->rows % d->gate_rows == 0);
+}
+
+// Threads that share a row (0: the block's) and eight-channel units a thread:
+// the least idle shape of those the kernels are built for.  Single-channel
+// loads (C not a multiple of 8) want 16 threads side by side.
+struct RowShape {
+    int tpr, units, threads;
+};
+RowShape row_shape(int C, bool vec, int max_units) {
+    const int n = (int)up(C, 8);
+    for (int tpr = vec ? 4 : 16; tpr <= 32; tpr *= 2)
+        for (int u = 1; u <= max_units; ++u)
+            if (tpr * u >= n) return {tpr, u, 128};
+    const int u = n > 512 ? 2 : 1;
+    return {0, u, (int)up(up(n, u), 32) * 32};
+}
+
+template <typename T, bool V, int TPR>
+void norm_fwd_units(const NormFwd& p, const RowShape& s, int grid, cudaStream_t st) {
+    switch (s.units) {
+        case 1: norm_fwd_kernel<T, V, TPR, 1><<<grid, s.threads, 0, st>>>(p); break;
+        case 2: norm_fwd_kernel<T, V, TPR, 2><<<grid, s.threads, 0, st>>>(p); break;
+        default:
+            if constexpr (TPR != 0) norm_fwd_kernel<T, V, TPR, 3><<<grid, s.threads, 0, st>>>(p);
+    }
+}
+
+template <typename T, bool V>
+void norm_fwd_shape(const NormFwd& p, cudaStream_t st) {
+    const RowShape s = row_shape(p.C, V, 3);
+    const long long rpb = s.tpr == 0 ? 1 : s.threads / s.tpr;
+    const int grid = (int)std::min<long long>(up(p.rows, rpb), (long long)kSms * 64);
+    switch (s.tpr) {
+        case 4: if constexpr (V) norm_fwd_units<T, V, 4>(p, s, grid, st); break;
+        case 8: if constexpr (V) norm_fwd_units<T, V, 8>(p, s, grid, st); break;
+        case 16: norm_fwd_units<T, V, 16>(p, s, grid, st); break;
+        case 32: norm_fwd_units<T, V, 32>(p, s, grid, st); break;
+        default: norm_fwd_units<T, V, 0>(p, s, grid, st);
+    }
+}
+
+// Launch shape of the backward pass: blocks per gate group.
+struct BwdShape {
+    RowShape row;
+    long long groups, group_rows;
+    int blocks_per_group;
+};
+BwdShape bwd_shape(const ccv3d_norm_desc* d, bool gated) {
+    BwdShape b;
+    b.row = row_shape(d->C, d->C % 8 == 0, 2);
+    b.groups = gated ? d->rows / d->gate_rows : 1;
+    b.group_rows = gated ? d->gate_rows : d->rows;
+    // short groups: fewer rows side by side, so that no thread is left without one
+    if (b.row.tpr != 0)
+        while (b.row.threads > 32 && b.row.threads / 2 / b.row.tpr >= b.group_rows)
+            b.row.threads /= 2;
+    const long long rpb = b.row.tpr == 0 ? 1 : b.row.threads / b.row.tpr;
+    const long long most = std::max<long long>(1, (long long)kSms * 8 / b.groups);
+    b.blocks_per_group = (int)std::max<long long>(1, std::min(most, up(b.group_rows, rpb * 4)));
+    return b;
+}
+
+template <typename T, bool V, int TPR, bool B>
+void norm_bwd_units(const NormBwd& p, const BwdShape& s, int grid, cudaStream_t st) {
+    const size_t smem = TPR == 0 ? 0 : (size_t)(s.row.threads / 32) * p.C * 4;
+    if (s.row.units == 1)
+        norm_bwd_kernel<T, V, TPR, 1, B><<<grid, s.row.threads, smem, st>>>(p);
+    else
+        norm_bwd_kernel<T, V, TPR, 2, B><<<grid, s.row.threads, smem, st>>>(p);
+}
+
+template <typename T, bool V, bool B>
+void norm_bwd_shape(const NormBwd& p, const BwdShape& s, int grid, cudaStream_t st) {
+    switch (s.row.tpr) {
+        case 4: if constexpr (V) norm_bwd_units<T, V, 4, B>(p, s, grid, st); break;
+        case 8: if constexpr (V) norm_bwd_units<T, V, 8, B>(p, s, grid, st); break;
+        case 16: norm_bwd_units<T, V, 16, B>(p, s, grid, st); break;
+        case 32: norm_bwd_units<T, V, 32, B>(p, s, grid, st); break;
+        default: norm_bwd_units<T, V, 0, B>(p, s, grid, st);
+    }
+}
+
+template <typename T>
+void norm_bwd_type(const NormBwd& p, const BwdShape& s, bool bias, int grid, cudaStream_t st) {
+    if (p.C % 8 == 0)
+        bias ? norm_bwd_shape<T, true, true>(p, s, grid, st)
+             : norm_bwd_shape<T, true, false>(p, s, grid, st);
+    else
+        bias ? norm_bwd_shape<T, false, true>(p, s, grid, st)
+             : norm_bwd_shape<T, false, false>(p, s, grid, st);
+}
+
+// --------------------------------------------------------------- pointwise
+ccv3d_status check_pointwise(const ccv3d_pointwise_desc* d) {
+    if (d == nullptr) return CCV3D_ERR_INVALID;
+    if (!known(d->dtype) || d->act < CCV3D_ACT_NONE || d->act > CCV3D_ACT_GELU)
+        return CCV3D_ERR_UNSUPPORTED;
+    if (d->pixels < 0 || d->Cin < 1 || d->Cout < 1) return CCV3D_ERR_INVALID;
+    if (d->pixels > 0x7fffffffLL - 256 || d->Cin > 65536 || d->Cout > 65536)
+        return CCV3D_ERR_UNSUPPORTED;
+    return CCV3D_OK;
+}
+
+size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Splits of the reduction on FFMA: enough blocks for the SMs, each with at
+// least 8 steps of 16.
+int simt_splits(long long M, long long N, long long K) {
+    const long long tiles = up(M, kPwTile) * up(N, kPwTile);
+    return (int)std::max<long long>(1, std::min<long long>({2 * kSms / tiles, up(K, 128), 512}));
+}
+size_t simt_ws(long long M, long long N, long long K) {
+    const int s = simt_splits(M, N, K);
+    return s > 1 ? pad256((size_t)s * M * N * 4) : 0;
+}
+
+// Column sums of dP: chunks of rows, one row of partials each.
+struct SumShape {
+    int tpr, col_blocks;
+    long long chunk, chunks;
+};
+SumShape sum_shape(long long M, int N) {
+    SumShape s;
+    const int n = (int)up(N, 8);
+    s.tpr = 4;
+    while (s.tpr < 32 && s.tpr < n) s.tpr *= 2;
+    s.col_blocks = (int)up(n, s.tpr);
+    const long long rows = 256 / s.tpr;  // side by side in a block
+    const long long want = std::max<long long>(1, kSms * 8LL / s.col_blocks);
+    s.chunk = std::max(up(M, want), rows * 4);
+    s.chunks = std::max<long long>(1, up(M, s.chunk));
+    return s;
+}
+
+// Workspace of the backward pass, in this order: dP, column sums, partials.
+struct BwdWs {
+    size_t dp, sums, parts, total;
+};
+BwdWs backward_ws(const ccv3d_pointwise_desc* d) {
+    BwdWs w;
+    const size_t e = size_of(d->dtype);
+    w.dp = d->act != CCV3D_ACT_NONE ? pad256((size_t)d->pixels * d->Cout * e) : 0;
+    w.sums = pad256((size_t)sum_shape(d->pixels, d->Cout).chunks * d->Cout * 4);
+    w.parts = std::max(simt_ws(d->pixels, d->Cin, d->Cout), simt_ws(d->Cout, d->Cin, d->pixels));
+    w.total = w.dp + w.sums + w.parts;
+    return w;
+}
+
+// D = A B^T on FFMA with the forward epilogue (o.out of type T).
+template <typename T, bool AK, bool BK>
+ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb, long long M,
+                      int N, long long K, PwOut o, float* partial, cudaStream_t st) {
+    PwSimt p;
+    p.A = A;
+    p.B = B;
+    p.sam = AK ? lda : 1;
+    p.sak = AK ? 1 : lda;
+    p.sbn = BK ? ldb : 1;
+    p.sbk = BK ? 1 : ldb;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    const int per16 = 16 / (int)sizeof(T);
+    p.vec = lda % per16 == 0 && ldb % per16 == 0;
+    p.splits = simt_splits(M, N, K);
+    p.k_per_split = up(up(K, p.splits), kPwK) * kPwK;
+    p.splits = (int)std::max<long long>(1, up(K, p.k_per_split));
+    p.o = o;
+    p.o.partial = p.splits > 1 ? partial : nullptr;
+    const long long tiles = up(M, kPwTile) * up(N, kPwTile);
+    if (tiles > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;
+    pw_simt_kernel<T, AK, BK><<<dim3((unsigned)tiles, 1, p.splits), 256, 0, st>>>(p);
+    if (p.splits > 1) {
+        const long long blocks = std::min<long long>(up(M * N, 256), kSms * 16LL);
+        pw_join_kernel<T><<<(unsigned)blocks, 256, 0, st>>>(partial, p.splits, o);
+    }
+    return launched();
+}
+
+template <typename T, int MR, int CPW>
+void run_rows(const T* x, const T* w, int K, const PwOut& o, cudaStream_t st) {
+    const unsigned grid = (unsigned)up(o.N, 4 * CPW);
+    if (K % 8 == 0) pw_rows_kernel<T, MR, CPW, true><<<grid, 128, 0, st>>>(x, w, K, o);
+    else pw_rows_kernel<T, MR, CPW, false><<<grid, 128, 0, st>>>(x, w, K, o);
+}
+
+template <typename T>
+ccv3d_status forward_type(const ccv3d_pointwise_desc* d, const void* x, const void* w,
+                          const PwOut& o, void* ws, cudaStream_t st) {
+    if (d->pixels <= kPwFewRows) {
+        const T *xt = static_cast<const T*>(x), *wt = static_cast<const T*>(w);
+        if (d->pixels == 1) run_rows<T, 1, 1>(xt, wt, d->Cin, o, st);
+        else if (d->pixels <= 4) run_rows<T, 4, 4>(xt, wt, d->Cin, o, st);
+        else run_rows<T, 8, 4>(xt, wt, d->Cin, o, st);
+        return launched();
+    }
+    return run_simt<T, true, true>(x, w, d->Cin, d->Cin, d->pixels, d->Cout, d->Cin, o,
+                                   static_cast<float*>(ws), st);
+}
+
+template <typename T>
+ccv3d_status backward_type(const ccv3d_pointwise_desc* d, const void* x, const void* w,
+                           const void* pre, const void* dout, void* dx, void* dw, void* dbias,
+                           void* ws, cudaStream_t st) {
+    const long long M = d->pixels;
+    const int K = d->Cin, N = d->Cout;
+    const BwdWs b = backward_ws(d);
+    uint8_t* at = static_cast<uint8_t*>(ws);
+    T* dp = reinterpret_cast<T*>(at);
+    float* sums = reinterpret_cast<float*>(at + b.dp);
+    float* parts = reinterpret_cast<float*>(at + b.dp + b.sums);
+    const bool make = d->act != CCV3D_ACT_NONE && (dx != nullptr || dw != nullptr);
+    if (make || dbias != nullptr) {
+        const SumShape s = sum_shape(M, N);
+        const dim3 grid(s.col_blocks, (unsigned)s.chunks);
+        const T* tp = static_cast<const T*>(pre);
+        const T* td = static_cast<const T*>(dout);
+        float* cs = dbias != nullptr ? sums : nullptr;
+        T* tdp = make ? dp : nullptr;
+        if (N % 8 == 0)
+            pw_dact_kernel<T, true><<<grid, 256, 0, st>>>(tp, td, tdp, cs, M, N, N, d->act, s.tpr,
+                                                         s.chunk);
+        else
+            pw_dact_kernel<T, false><<<grid, 256, 0, st>>>(tp, td, tdp, cs, M, N, N, d->act, s.tpr,
+                                                          s.chunk);
+        if (dbias != nullptr)
+            pw_colsum_kernel<T><<<(unsigned)up(N, 32), dim3(32, 32), 0, st>>>(
+                sums, (int)s.chunks, N, static_cast<T*>(dbias));
+        if (launched() != CCV3D_OK) return CCV3D_ERR_CUDA;
+    }
+    const void* dP = make ? dp : dout;
+    PwOut o = {};
+    o.act = CCV3D_ACT_NONE;
+    ccv3d_status r = CCV3D_OK;
+    if (dx != nullptr) {
+        o.out = dx;
+        o.M = M;
+        o.N = K;
+        r = run_simt<T, true, false>(dP, w, N, K, M, K, N, o, parts, st);
+    }
+    if (r == CCV3D_OK && dw != nullptr) {
+        o.out = dw;
+        o.M = N;
+        o.N = K;
+        r = run_simt<T, false, false>(dP, x, N, K, N, K, M, o, parts, st);
+    }
+    return r;
+}
+
+// ------------------------------------------------------------ quantised cache
+ccv3d_status check_qcache(const ccv3d_qcache_desc* d) {
+    if (d == nullptr) return CCV3D_ERR_INVALID;
+    if (!known(d->dtype) || d->format < CCV3D_Q_INT8 || d->format > CCV3D_Q_E2M1)
+        return CCV3D_ERR_UNSUPPORTED;
+    if (d->N < 0 || d->C < 1 || d->H < 1 || d->W < 1 || d->ring_slots < 1)
+        return CCV3D_ERR_INVALID;
+    if (d->C > 65536 || (long long)d->H * d->W > 0x7fffffffLL ||
+        (long long)d->N * d->ring_slots > 0x7fffffffLL ||
+        (double)d->N * d->ring_slots * d->H * d->W * d->C > 7e13)
+        return CCV3D_ERR_UNSUPPORTED;
+    return CCV3D_OK;
+}
+
+QCacheJob qcache_job(const ccv3d_qcache_desc* d) {
+    QCacheJob j = {};
+    j.pixels = (long long)d->H * d->W;
+    j.N = d->N;
+    j.C = d->C;
+    j.groups = (d->C + kQGroup - 1) / kQGroup;
+    j.code_bytes = d->format == CCV3D_Q_E2M1 ? (d->C + 1) / 2 : d->C;
+    j.slots = d->ring_slots;
+    return j;
+}
+
+// Whole frames on the grid's second axis (at most 65535 of them).
+dim3 qcache_grid(const QCacheJob& j, long long threads_a_pixel) {
+    const long long frames = (long long)j.N * j.frames;
+    const long long want = std::max<long long>(1, kSms * 32LL / frames);
+    return dim3((unsigned)std::min<long long>(up(j.pixels * threads_a_pixel, 256), want),
+                (unsigned)frames);
+}
+
+}  // namespace
+
+extern "C" {
+
+ccv3d_status ccv3d_norm_forward(const ccv3d_norm_desc* d, const void* h, const void* b,
+                                const void* gate, const void* post_w, const void* post_bias,
+                                const void* pre_w, const void* pre_bias, void* h_out, void* y,
+                                cudaStream_t stream) {
+    const ccv3d_status c = check_norm(d);
+    if (c != CCV3D_OK) return c;
+    const bool pre = d->pre != CCV3D_NORM_NONE, post = d->post != CCV3D_NORM_NONE;
+    if (!gate_fits(d, gate)) return CCV3D_ERR_INVALID;
+    if (d->rows == 0) return CCV3D_OK;  // (empty tensors have NULL addresses)
+    if ((b == nullptr && (!pre || post || gate != nullptr || h_out != nullptr)) ||
+        (!post && (post_w != nullptr || post_bias != nullptr)) ||
+        (!pre && (pre_w != nullptr || pre_bias != nullptr || y != nullptr)))
+        return CCV3D_ERR_INVALID;
+    if (h == nullptr || (b != nullptr && h_out == nullptr) || (pre && y == nullptr))
+        return CCV3D_ERR_INVALID;
+    const size_t e = size_of(d->dtype), vec = d->C * e, all = (size_t)d->rows * vec;
+    Buffers bufs;
+    if (h != h_out) bufs.in(h, all);  // the stream may be updated in place
+    bufs.in(b, all);
+    if (gate != nullptr) bufs.in(gate, (size_t)(d->rows / d->gate_rows) * vec);
+    for (const void* v : {post_w, post_bias, pre_w, pre_bias}) bufs.in(v, vec);
+    bufs.out(h_out, all);
+    bufs.out(y, all);
+    const ccv3d_status k = bufs.check();
+    if (k != CCV3D_OK) return k;
+    const NormFwd p = {h, b, gate, post_w, post_bias, pre_w, pre_bias, h_out, y,
+                       d->rows, gate != nullptr ? d->gate_rows : 1, d->C, d->pre, d->post, d->act,
+                       d->eps, d->scale, 1.0f / (float)d->C};
+    const bool v = d->C % 8 == 0;
+    if (d->dtype == CCV3D_BF16)
+        v ? norm_fwd_shape<bf16, true>(p, stream) : norm_fwd_shape<bf16, false>(p, stream);
+    else
+        v ? norm_fwd_shape<float, true>(p, stream) : norm_fwd_shape<float, false>(p, stream);
+    return launched();
+}
+
+size_t ccv3d_norm_workspace(const ccv3d_norm_desc* d) {
+    if (check_norm(d) != CCV3D_OK || d->rows == 0) return 0;
+    // a call with a gate and one without may both follow: the larger of the two
+    long long slots = 0;
+    for (int gated = 0; gated < 2; ++gated) {
+        if (gated && (d->gate_rows < 1 || d->rows % d->gate_rows != 0)) continue;
+        const BwdShape b = bwd_shape(d, gated != 0);
+        slots = std::max(slots, b.groups * b.blocks_per_group);
+    }
+    return (size_t)slots * d->C * 4 * sizeof(float);
+}
+
+ccv3d_status ccv3d_norm_backward(const ccv3d_norm_desc* d, const void* h_out, const void* b,
+                                 const void* gate, const void* post_w, const void* post_bias,
+                                 const void* pre_w, const void* pre_bias, const void* dy,
+                                 const void* dh_out, void* dh, void* db, void* dgate,
+                                 void* dpost_w, void* dpost_bias, void* dpre_w, void* dpre_bias,
+                                 void* ws, size_t ws_bytes, cudaStream_t stream) {
+    const ccv3d_status c = check_norm(d);
+    if (c != CCV3D_OK) return c;
+    const bool pre = d->pre != CCV3D_NORM_NONE, post = d->post != CCV3D_NORM_NONE;
+    if (!gate_fits(d, gate)) return CCV3D_ERR_INVALID;
+    const size_t e = size_of(d->dtype), vec = d->C * e, all = (size_t)d->rows * vec;
+    if (d->rows == 0) {  // sums over no rows
+        for (void* v : {dpost_w, dpost_bias, dpre_w, dpre_bias})
+            if (v != nullptr && cudaMemsetAsync(v, 0, vec, stream) != cudaSuccess) {
+                cudaGetLastError();
+                return CCV3D_ERR_CUDA;
+            }
+        return CCV3D_OK;
+    }
+    if ((b == nullptr && (!pre || post || gate != nullptr || db != nullptr)) ||
+        (!post && (post_w != nullptr || post_bias != nullptr)) ||
+        (!pre && (pre_w != nullptr || pre_bias != nullptr || dy != nullptr)) ||
+        (gate == nullptr && dgate != nullptr) || (post_w == nullptr && dpost_w != nullptr) ||
+        (post_bias == nullptr && dpost_bias != nullptr) ||
+        (pre_w == nullptr && dpre_w != nullptr) || (pre_bias == nullptr && dpre_bias != nullptr))
+        return CCV3D_ERR_INVALID;
+    if ((pre && (h_out == nullptr || dy == nullptr)) || (dy == nullptr && dh_out == nullptr))
+        return CCV3D_ERR_INVALID;
+    const bool sums = dgate != nullptr || dpost_w != nullptr || dpost_bias != nullptr ||
+                      dpre_w != nullptr || dpre_bias != nullptr;
+    const size_t need = sums ? ccv3d_norm_workspace(d) : 0;
+    if (sums && ws == nullptr) return CCV3D_ERR_INVALID;
+    if (ws_bytes < need) return CCV3D_ERR_SCRATCH_LIMIT;
+    const size_t gates = gate != nullptr ? (size_t)(d->rows / d->gate_rows) * vec : 0;
+    Buffers bufs;
+    for (const void* v : {h_out, b, dy, dh_out}) bufs.in(v, all);
+    for (const void* v : {post_w, post_bias, pre_w, pre_bias}) bufs.in(v, vec);
+    bufs.in(gate, gates);
+    bufs.out(dh, all);
+    bufs.out(db, all);
+    bufs.out(dgate, gates);
+    for (const void* v : {dpost_w, dpost_bias, dpre_w, dpre_bias}) bufs.out(v, vec);
+    bufs.out(ws, need);
+    const ccv3d_status k = bufs.check();
+    if (k != CCV3D_OK) return k;
+    const BwdShape s = bwd_shape(d, gate != nullptr);
+    const long long slots = s.groups * s.blocks_per_group;
+    if (slots > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;
+    // sums of du and G are wanted for bias gradients, and for dgate where a bias adds to it
+    const bool bias = dpre_bias != nullptr || dpost_bias != nullptr ||
+                      (dgate != nullptr && post_bias != nullptr);
+    const NormBwd p = {h_out, b, gate, post_w, post_bias, pre_w, pre_bias, dy, dh_out, dh, db,
+                       sums ? static_cast<float*>(ws) : nullptr, d->rows, s.group_rows, s.groups,
+                       slots, s.blocks_per_group, d->C, d->pre, d->post, d->act, d->eps, d->scale,
+                       1.0f / (float)d->C};
+    if (d->dtype == CCV3D_BF16) norm_bwd_type<bf16>(p, s, bias, (int)slots, stream);
+    else norm_bwd_type<float>(p, s, bias, (int)slots, stream);
+    if (launched() != CCV3D_OK) return CCV3D_ERR_CUDA;
+    if (!sums) return CCV3D_OK;
+    float* part = static_cast<float*>(ws);
+    const NormFin f = {part, part, gate, post_w, post_bias, dgate, dpost_w, dpost_bias, dpre_w,
+                       dpre_bias, s.groups, slots, s.blocks_per_group, d->C, bias ? 1 : 0,
+                       b != nullptr ? 1 : 0, d->scale};
+    const dim3 grid((unsigned)up(d->C, 32), (unsigned)std::min<long long>(s.groups, 32768));
+    const dim3 block(32, 32);
+    if (d->dtype == CCV3D_BF16) {
+        norm_fin_group_kernel<bf16><<<grid, block, 0, stream>>>(f);
+        if (s.groups > 1) norm_fin_all_kernel<bf16><<<grid.x, block, 0, stream>>>(f);
+    } else {
+        norm_fin_group_kernel<float><<<grid, block, 0, stream>>>(f);
+        if (s.groups > 1) norm_fin_all_kernel<float><<<grid.x, block, 0, stream>>>(f);
+    }
+    return launched();
+}
+
+ccv3d_status ccv3d_pointwise_workspace(const ccv3d_pointwise_desc* d, size_t* forward_bytes,
+                                       size_t* backward_bytes) {
+    if (forward_bytes) *forward_bytes = 0;
+    if (backward_bytes) *backward_bytes = 0;
+    const ccv3d_status c = check_pointwise(d);
+    if (c != CCV3D_OK) return c;
+    if (d->pixels == 0) return CCV3D_OK;
+    if (forward_bytes)
+        *forward_bytes = d->pixels <= kPwFewRows ? 0 : simt_ws(d->pixels, d->Cout, d->Cin);
+    if (backward_bytes) *backward_bytes = backward_ws(d).total;
+    return CCV3D_OK;
+}
+
+ccv3d_status ccv3d_pointwise_forward(const ccv3d_pointwise_desc* d, const void* x, const void* w,
+                                     const void* bias, const void* residual, void* out, void* pre,
+                                     void* ws, size_t ws_bytes, cudaStream_t stream) {
+    size_t need = 0;
+    const ccv3d_status c = ccv3d_pointwise_workspace(d, &need, nullptr);
+    if (c != CCV3D_OK) return c;
+    if (d->pixels == 0) return CCV3D_OK;
+    if (x == nullptr || w == nullptr || out == nullptr || (need > 0 && ws == nullptr))
+        return CCV3D_ERR_INVALID;
+    if (ws_bytes < need) return CCV3D_ERR_SCRATCH_LIMIT;
+    const size_t e = size_of(d->dtype), o_bytes = (size_t)d->pixels * d->Cout * e;
+    Buffers bufs;
+    bufs.in(x, (size_t)d->pixels * d->Cin * e);
+    bufs.in(w, (size_t)d->Cout * d->Cin * e);
+    bufs.in(bias, (size_t)d->Cout * e);
+    if (residual != out) bufs.in(residual, o_bytes);  // the stream may be updated in place
+    bufs.out(out, o_bytes);
+    bufs.out(pre, o_bytes);
+    bufs.out(ws, need);
+    const ccv3d_status k = bufs.check();
+    if (k != CCV3D_OK) return k;
+    PwOut o = {bias, residual, out, pre, nullptr, d->pixels, d->Cout, d->act};
+    return d->dtype == CCV3D_BF16 ? forward_type<bf16>(d, x, w, o, ws, stream)
+                                  : forward_type<float>(d, x, w, o, ws, stream);
+}
+
+ccv3d_status ccv3d_pointwise_backward(const ccv3d_pointwise_desc* d, const void* x, const void* w,
+                                      const void* pre, const void* dout, void* dx, void* dw,
+                                      void* dbias, void* ws, size_t ws_bytes,
+                                      cudaStream_t stream) {
+    size_t need = 0;
+    const ccv3d_status c = ccv3d_pointwise_workspace(d, nullptr, &need);
+    if (c != CCV3D_OK) return c;
+    const size_t e = size_of(d->dtype);
+    if (d->pixels == 0) {
+        cudaError_t r = cudaSuccess;
+        if (dw != nullptr) r = cudaMemsetAsync(dw, 0, (size_t)d->Cout * d->Cin * e, stream);
+        if (r == cudaSuccess && dbias != nullptr)
+            r = cudaMemsetAsync(dbias, 0, (size_t)d->Cout * e, stream);
+        if (r != cudaSuccess) cudaGetLastError();
+        return r == cudaSuccess ? CCV3D_OK : CCV3D_ERR_CUDA;
+    }
+    if (dout == nullptr || (dx != nullptr && w == nullptr) || (dw != nullptr && x == nullptr) ||
+        (pre != nullptr) != (d->act != CCV3D_ACT_NONE) || (need > 0 && ws == nullptr))
+        return CCV3D_ERR_INVALID;
+    if (ws_bytes < need) return CCV3D_ERR_SCRATCH_LIMIT;
+    const size_t x_bytes = (size_t)d->pixels * d->Cin * e, w_bytes = (size_t)d->Cout * d->Cin * e,
+                 o_bytes = (size_t)d->pixels * d->Cout * e;
+    Buffers bufs;
+    bufs.in(x, x_bytes);
+    bufs.in(w, w_bytes);
+    bufs.in(pre, o_bytes);
+    bufs.in(dout, o_bytes);
+    bufs.out(dx, x_bytes);
+    bufs.out(dw, w_bytes);
+    bufs.out(dbias, (size_t)d->Cout * e);
+    bufs.out(ws, need);
+    const ccv3d_status k = bufs.check();
+    if (k != CCV3D_OK) return k;
+    return d->dtype == CCV3D_BF16
+               ? backward_type<bf16>(d, x, w, pre, dout, dx, dw, dbias, ws, stream)
+               : backward_type<float>(d, x, w, pre, dout, dx, dw, dbias, ws, stream);
+}
+
+ccv3d_status ccv3d_qcache_sizes(const ccv3d_qcache_desc* d, size_t* code_bytes,
+                                size_t* scale_bytes) {
+    if (code_bytes) *code_bytes = 0;
+    if (scale_bytes) *scale_bytes = 0;
+    const ccv3d_status c = check_qcache(d);
+    if (c != CCV3D_OK) return c;
+    const QCacheJob j = qcache_job(d);
+    const size_t px = (size_t)d->N * d->ring_slots * j.pixels;
+    if (code_bytes) *code_bytes = px * j.code_bytes;
+    if (scale_bytes) *scale_bytes = px * j.groups;
+    return CCV3D_OK;
+}
+
+ccv3d_status ccv3d_qcache_write(const ccv3d_qcache_desc* d, const void* x, int T_x, int first,
+                                int frames, int slot, void* codes, void* scales,
+                                cudaStream_t stream) {
+    size_t cb = 0, sb = 0;
+    const ccv3d_status c = ccv3d_qcache_sizes(d, &cb, &sb);
+    if (c != CCV3D_OK) return c;
+    if (T_x < 0 || first < 0 || frames < 0 || frames > T_x - first || frames > d->ring_slots ||
+        slot < 0 || slot >= d->ring_slots)
+        return CCV3D_ERR_INVALID;
+    if ((long long)d->N * frames == 0) return CCV3D_OK;
+    if (x == nullptr || codes == nullptr || scales == nullptr) return CCV3D_ERR_INVALID;
+    if ((long long)d->N * frames > 65535) return CCV3D_ERR_UNSUPPORTED;
+    QCacheJob j = qcache_job(d);
+    Buffers bufs;
+    bufs.in(x, (size_t)d->N * T_x * j.pixels * d->C * size_of(d->dtype));
+    bufs.out(codes, cb);
+    bufs.out(scales, sb);
+    const ccv3d_status k = bufs.check();
+    if (k != CCV3D_OK) return k;
+    j.src = x;
+    j.codes = static_cast<uint8_t*>(codes);
+    j.scales = static_cast<uint8_t*>(scales);
+    j.T = T_x;
+    j.first = first;
+    j.frames = frames;
+    j.slot = slot;
+    const dim3 grid = qcache_grid(j, 4LL * j.groups);
+    const bool v = d->C % 8 == 0;
+    if (d->dtype == CCV3D_BF16) {
+        if (v) qcache_write_kernel<bf16, true><<<grid, 256, 0, stream>>>(j, d->format);
+        else qcache_write_kernel<bf16, false><<<grid, 256, 0, stream>>>(j, d->format);
+    } else {
+        if (v) qcache_write_kernel<float, true><<<grid, 256, 0, stream>>>(j, d->format);
+        else qcache_write_kernel<float, false><<<grid, 256, 0, stream>>>(j, d->format);
+    }
+    return launched();
+}
+
+ccv3d_status ccv3d_qcache_read(const ccv3d_qcache_desc* d, const void* codes, const void* scales,
+                               int head, int frames, void* out, cudaStream_t stream) {
+    size_t cb = 0, sb = 0;
+    const ccv3d_status c = ccv3d_qcache_sizes(d, &cb, &sb);
+    if (c != CCV3D_OK) return c;
+    if (frames < 0 || frames > d->ring_slots || head < 0 || head >= d->ring_slots)
+        return CCV3D_ERR_INVALID;
+    if ((long long)d->N * frames == 0) return CCV3D_OK;
+    if (out == nullptr || codes == nullptr || scales == nullptr) return CCV3D_ERR_INVALID;
+    if ((long long)d->N * frames > 65535) return CCV3D_ERR_UNSUPPORTED;
+    QCacheJob j = qcache_job(d);
+    Buffers bufs;
+    bufs.in(codes, cb);
+    bufs.in(scales, sb);
+    bufs.out(out, (size_t)d->N * frames * j.pixels * d->C * size_of(d->dtype));
+    const ccv3d_status k = bufs.check();
+    if (k != CCV3D_OK) return k;
+    j.dst = out;
+    j.codes = static_cast<uint8_t*>(const_cast<void*>(codes));
+    j.scales = static_cast<uint8_t*>(const_cast<void*>(scales));
+    j.frames = frames;
+    j.slot = head;
+    const dim3 grid = qcache_grid(j, up(d->C, 8));
+    const bool v = d->C % 8 == 0;
+    if (d->dtype == CCV3D_BF16) {
+        if (v) qcache_read_kernel<bf16, true><<<grid, 256, 0, stream>>>(j, d->format);
+        else qcache_read_kernel<bf16, false><<<grid, 256, 0, stream>>>(j, d->format);
+    } else {
+        if (v) qcache_read_kernel<float, true><<<grid, 256, 0, stream>>>(j, d->format);
+        else qcache_read_kernel<float, false><<<grid, 256, 0, stream>>>(j, d->format);
+    }
+    return launched();
+}
+
+ccv3d_status ccv3d_block_get_status(cudaStream_t stream) {
+    int v = 0;
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_block_status, sizeof(int), 0,
+                                              cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess && v != 0) {
+        e = cudaMemcpyToSymbolAsync(g_block_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice,
+                                    stream);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return CCV3D_ERR_CUDA;
+    }
+    return static_cast<ccv3d_status>(v);
+}
+
+}  // extern "C"

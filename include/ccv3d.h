@@ -60,8 +60,10 @@
 extern "C" {
 #endif
 
-#define CCV3D_ABI_VERSION 2 /* 2: ccv3d_stats.plans_unsupported, stream-scoped status
-                               reads, ring-buffer caches */
+#define CCV3D_ABI_VERSION 3 /* 2: ccv3d_stats.plans_unsupported, stream-scoped status
+                               reads, ring-buffer caches; 3: the operators around
+                               the convolution (ccv3d_norm_*, ccv3d_pointwise_*,
+                               ccv3d_qcache_*, ccv3d_forward_qring) */
 #define CCV3D_MAX_KT 3 /* the contract's temporal kernel size */
 
 typedef enum { CCV3D_BF16 = 0, CCV3D_FP32 = 1 } ccv3d_dtype;
@@ -79,8 +81,10 @@ typedef enum {
                                    overlaps an input */
     CCV3D_ERR_CUDA = 6,         /* a CUDA runtime/driver call failed */
     CCV3D_ERR_TIMEOUT = 7,      /* a bounded device-side wait ran out */
-    CCV3D_ERR_SCRATCH_LIMIT = 8, /* ccv3d_forward_noalloc: the call needs more
-                                    device scratch than its fixed array holds */
+    CCV3D_ERR_SCRATCH_LIMIT = 8, /* the call needs more device scratch than there is:
+                                    ccv3d_forward_noalloc's fixed array, or the
+                                    workspace given to a ccv3d_norm_* or
+                                    ccv3d_pointwise_* call */
     CCV3D_ERR_BOUNDS = 9         /* bounds-checked build (libccv3d_checked.so)
                                     only: a kernel computed an address outside
                                     the buffer it indexes; the access was
@@ -289,6 +293,193 @@ CCV3D_API ccv3d_status ccv3d_selftest_bounds(cudaStream_t stream);
  * ALIAS (the buffers overlap), CUDA (launch failure).  n == 0 does nothing. */
 CCV3D_API ccv3d_status ccv3d_quantize_u8(const void* in, ccv3d_dtype dtype, void* out,
                                          long long n, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The operators around the convolution: a decoder's residual block is
+ *   norm -> act -> conv3d(cache) -> norm -> act -> conv3d(cache) -> + shortcut.
+ *
+ * All of them work on the convolution's layout (channels innermost; a row is
+ * the C channels of one pixel, rows dense and in any order), in its element
+ * types, and as its calls do: every buffer is the caller's, device pointers of
+ * the current device, 16-byte aligned (vectors of C channels too); the call is
+ * asynchronous on `stream`, never synchronises, allocates nothing, checks its
+ * arguments before any device work, and can be captured into a CUDA graph.  A
+ * workspace holds nothing from one call to the next; calls that may overlap on
+ * the GPU (other streams, or graphs holding them) each need their own.
+ *
+ * Errors, besides those named at each: INVALID (NULL desc, an argument that
+ * has to be there and is NULL or has to be NULL and is not, a size out of
+ * range), UNSUPPORTED (unknown dtype, kind or format; sizes past the stated
+ * limits), ALIGNMENT, ALIAS (an output overlaps another buffer of the call),
+ * SCRATCH_LIMIT (the workspace is smaller than the size asked for), CUDA.
+ * Sizes of zero rows, pixels or frames do nothing (gradients summed over no
+ * rows are zeros).  A device-side timeout (see ccv3d_block_get_status) is the
+ * only error found after the call returned. */
+typedef enum { CCV3D_NORM_NONE = 0, CCV3D_NORM_RMS = 1, CCV3D_NORM_LAYER = 2 } ccv3d_norm_kind;
+typedef enum {
+    CCV3D_ACT_NONE = 0,
+    CCV3D_ACT_SILU = 1, /* u / (1 + exp(-u)) */
+    CCV3D_ACT_GELU = 2  /* 0.5 u (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))) */
+} ccv3d_act;
+
+#define CCV3D_NORM_MAX_C 8192
+
+/* Norms before and after a block, fused with its gate and residual scale:
+ *   h_out = h + scale * gate * post(b),    y = act(pre(h_out)),
+ * per row v: RMS   norm(v) = v / sqrt(mean(v^2) + eps) * w + bias,
+ *            LAYER norm(v) = (v - mean(v)) / sqrt(var(v) + eps) * w + bias
+ * (var biased).  h is the residual stream, b the block's output, post the norm
+ * after that block, pre the norm (and act) before the next one.  h_out is
+ * rounded to the element type first and y is the norm of what is stored, so
+ * the call gives the bits of its two halves called one after the other. */
+typedef struct {
+    long long rows;       /* pixels: N * T * H * W, >= 0 */
+    int C;                /* channels, 1 .. CCV3D_NORM_MAX_C */
+    ccv3d_norm_kind pre;  /* NONE: no y */
+    ccv3d_norm_kind post; /* NONE: b is added as it is */
+    ccv3d_act act;
+    float eps;            /* > 0, finite */
+    float scale;          /* residual scale, finite */
+    long long gate_rows;  /* consecutive rows that share a row of the gate (all
+                             rows: one gate; H*W: one per frame); rows must be a
+                             multiple of it; ignored without a gate */
+    ccv3d_dtype dtype;    /* of every tensor and vector; sums are fp32 */
+} ccv3d_norm_desc;
+
+/* Forward.  h [rows, C]; b [rows, C] or NULL (then y = act(pre(h)), and gate,
+ * post_w, post_bias and h_out are NULL, post NONE); gate [rows / gate_rows, C]
+ * or NULL (ones); post_w, post_bias, pre_w, pre_bias [C] or NULL (ones, zeros;
+ * NULL where the norm is NONE); h_out [rows, C], wanted with b; y [rows, C],
+ * wanted iff pre is not NONE.  h_out may be h itself (the stream updated in
+ * place); otherwise outputs overlap nothing. */
+CCV3D_API ccv3d_status ccv3d_norm_forward(const ccv3d_norm_desc* desc, const void* h,
+                                          const void* b, const void* gate, const void* post_w,
+                                          const void* post_bias, const void* pre_w,
+                                          const void* pre_bias, void* h_out, void* y,
+                                          cudaStream_t stream);
+
+/* Bytes of workspace ccv3d_norm_backward needs (0 for a refused desc). */
+CCV3D_API size_t ccv3d_norm_workspace(const ccv3d_norm_desc* desc);
+
+/* Gradients of the forward call.  h_out is the value the forward call stored
+ * (h itself without b); dy and dh_out are the gradients of y (NULL iff pre is
+ * NONE) and of h_out (NULL: zero).  dh, db, dgate, dpost_w, dpost_bias, dpre_w
+ * and dpre_bias receive the gradients of what they are named after, in its
+ * shape; NULL where it is not wanted (and where there is no such input: a
+ * gradient asked for of a NULL gate, weight or bias is INVALID).  ws: at least
+ * ccv3d_norm_workspace bytes, 16-byte aligned; may be NULL when no gradient of
+ * a vector is asked for.  Sums are taken in a fixed order: the same bits every
+ * run. */
+CCV3D_API ccv3d_status ccv3d_norm_backward(const ccv3d_norm_desc* desc, const void* h_out,
+                                           const void* b, const void* gate, const void* post_w,
+                                           const void* post_bias, const void* pre_w,
+                                           const void* pre_bias, const void* dy,
+                                           const void* dh_out, void* dh, void* db, void* dgate,
+                                           void* dpost_w, void* dpost_bias, void* dpre_w,
+                                           void* dpre_bias, void* ws, size_t ws_bytes,
+                                           cudaStream_t stream);
+
+/* The 1x1x1 convolution (shortcuts, qkv, projections), a matrix product with
+ * bias, activation and residual in its epilogue:
+ *   u = x w^T + bias,   out = act(u) + residual,   pre = u. */
+typedef struct {
+    long long pixels;  /* rows of x, 0 .. 2^31 - 257 */
+    int Cin, Cout;     /* 1 .. 65536 */
+    ccv3d_act act;
+    ccv3d_dtype dtype; /* BF16: bf16 in, fp32 accumulate and epilogue, one rounding
+                          to bf16 out; FP32: IEEE fp32 FMA, no TF32 */
+} ccv3d_pointwise_desc;
+
+/* Bytes of workspace the forward and the backward call need (may be 0; any
+ * pointer may be NULL).  Errors: INVALID, UNSUPPORTED. */
+CCV3D_API ccv3d_status ccv3d_pointwise_workspace(const ccv3d_pointwise_desc* desc,
+                                                 size_t* forward_bytes, size_t* backward_bytes);
+
+/* Forward.  x [pixels, Cin]; w [Cout, Cin]; bias [Cout] or NULL; residual
+ * [pixels, Cout] or NULL; out [pixels, Cout]; pre [pixels, Cout] or NULL
+ * receives u rounded to the element type, for the backward call (out is taken
+ * from the unrounded u).  residual may be out itself; otherwise outputs overlap
+ * nothing.  A NaN or infinity in a row of x or residual stays in that row. */
+CCV3D_API ccv3d_status ccv3d_pointwise_forward(const ccv3d_pointwise_desc* desc, const void* x,
+                                               const void* w, const void* bias,
+                                               const void* residual, void* out, void* pre,
+                                               void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Gradients: with dP = dout * act'(pre),
+ *   dx = dP w,   dw = dP^T x,   dbias = sum over pixels of dP;
+ * the residual's gradient is dout itself.  pre: as the forward call stored it,
+ * NULL iff act is NONE.  dx, dw, dbias: NULL where not wanted.  BF16: dP is
+ * rounded to bf16, the tensor cores' operand type (not for act NONE, where it
+ * is dout); dbias sums it unrounded.  Sums are taken in a fixed order: the
+ * same bits every run. */
+CCV3D_API ccv3d_status ccv3d_pointwise_backward(const ccv3d_pointwise_desc* desc, const void* x,
+                                                const void* w, const void* pre,
+                                                const void* dout, void* dx, void* dw,
+                                                void* dbias, void* ws, size_t ws_bytes,
+                                                cudaStream_t stream);
+
+/* A ring cache (ccv3d_forward_ring) held in 8 or 4 bits, so that the caches of
+ * a stream, or of many streams, take a half to a quarter of the memory.  32
+ * consecutive channels of a pixel (the last group of a pixel may be shorter)
+ * share a power-of-two scale; a code is the format's value nearest x / scale,
+ * ties to even; nothing saturates; a value read back is code * scale.  A group
+ * holding a NaN or an infinity reads back as NaN. */
+typedef enum {
+    CCV3D_Q_INT8 = 0, /* -127 .. 127 */
+    CCV3D_Q_E4M3 = 1, /* 8-bit float, largest 448 */
+    CCV3D_Q_E2M1 = 2  /* 4-bit float, largest 6; two per byte, the even channel low */
+} ccv3d_qformat;
+
+typedef struct {
+    int N, C, H, W;    /* batch entries, channels (<= 65536), spatial size */
+    int ring_slots;    /* frames the ring holds per batch entry, >= 1 */
+    ccv3d_qformat format;
+    ccv3d_dtype dtype; /* of the frames written and read */
+} ccv3d_qcache_desc;
+
+/* Bytes of the two buffers of a cache (any pointer may be NULL):
+ *   codes   [N, ring_slots, H, W, C]            (4 bits: (C + 1) / 2 bytes)
+ *   scales  [N, ring_slots, H, W, (C + 31) / 32]  byte c stands for 2^(c - 127)
+ * Errors: INVALID, UNSUPPORTED. */
+CCV3D_API ccv3d_status ccv3d_qcache_sizes(const ccv3d_qcache_desc* desc, size_t* code_bytes,
+                                          size_t* scale_bytes);
+
+/* Quantise frames first .. first + frames - 1 of x [N, T_x, H, W, C] into slots
+ * (slot + i) mod ring_slots.  frames <= ring_slots; no other slot changes. */
+CCV3D_API ccv3d_status ccv3d_qcache_write(const ccv3d_qcache_desc* desc, const void* x, int T_x,
+                                          int first, int frames, int slot, void* codes,
+                                          void* scales, cudaStream_t stream);
+
+/* Read slots (head + t) mod ring_slots, t < frames, back into
+ * out [N, frames, H, W, C]: a dense cache for ccv3d_forward. */
+CCV3D_API ccv3d_status ccv3d_qcache_read(const ccv3d_qcache_desc* desc, const void* codes,
+                                         const void* scales, int head, int frames, void* out,
+                                         cudaStream_t stream);
+
+/* ccv3d_forward_ring with the ring held in 8 or 4 bits: reads the plan's
+ * cache_len frames from head on into cache_buf ([N, cache_len, H, W, Cin], a
+ * scratch that any number of modules can share; NULL allowed iff cache_len is
+ * 0), runs the convolution on them, and quantises the n_w = min(K', T_x) last
+ * frames of x, K' = min(cache_keep, |Z|) with the plan's cache_keep, into the
+ * slots after the cached ones.  head, ring_slots, next_head and the order of
+ * slots are those of ccv3d_forward_ring; out is ccv3d_forward's on the cache as
+ * read back.  The plan must have been made for the desc's N, C, H, W and dtype
+ * (else INVALID). */
+CCV3D_API ccv3d_status ccv3d_forward_qring(ccv3d_plan_t plan, const void* x,
+                                           const ccv3d_qcache_desc* desc, void* codes,
+                                           void* scales, int head, void* cache_buf,
+                                           const void* w, const void* bias, void* out,
+                                           const int stride[2], const int pad[2],
+                                           const int dilation[3], cudaStream_t stream,
+                                           int* next_head);
+
+/* Status of the ccv3d_norm_*, ccv3d_pointwise_* and ccv3d_qcache_* calls on the
+ * current device: waits for the work queued on `stream`, then returns and
+ * clears the first error their kernels recorded on the device -- CCV3D_OK,
+ * CCV3D_ERR_TIMEOUT (a bounded wait of the tensor-core product ran out: that
+ * call's output is not valid) or, in the bounds-checked build,
+ * CCV3D_ERR_BOUNDS.  Allocates nothing.  Errors: CUDA. */
+CCV3D_API ccv3d_status ccv3d_block_get_status(cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Forward call that allocates nothing.

@@ -1,0 +1,135 @@
+"""The operators together, as a decoder's residual block uses them:
+    norm + SiLU -> conv3d (quantised ring cache) -> norm + SiLU -> conv3d -> + 1x1x1 shortcut,
+streamed frame by frame, against the same block in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from block_util import d, norm
+from causal_conv3d_video_b200 import ccv3d
+from causal_conv3d_video_b200.workloads import Conv
+from parity_util import assert_close, oracle_params
+from test_gpu_qcache import quantise
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "e2m1"])
+@pytest.mark.parametrize("Cin,Cout,H,W,T_x,dtype", [
+    (32, 48, 9, 14, 1, "bf16"), (64, 64, 12, 20, 2, "bf16"), (24, 16, 5, 7, 1, "fp32")])
+def test_forward_qring_streams(Cin, Cout, H, W, T_x, dtype, fmt):
+    """Each call's output is ccv3d_forward's on the cache as read back (the
+    oracle's on those values), and the ring holds the arriving frames' codes."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s, std=1.0: (torch.randn(s, device="cuda", generator=g) * std).to(
+        torch.bfloat16 if dtype == "bf16" else torch.float32)
+    w, b = rnd(Cout, 3, 3, 3, Cin, std=(27 * Cin) ** -0.5), rnd(Cout, std=0.1)
+    slots, keep = 2 + T_x, 2
+    desc = ccv3d.make_qcache_desc(N=1, H=H, W=W, C=Cin, ring_slots=slots, format=fmt, dtype=dtype)
+    codes, scales = ccv3d.alloc_qcache(desc)
+    head, kept = 1, []        # kept: the frames the cache should hold, as read back
+    for step in range(5):
+        conv = Conv("s", Cin, Cout, H, W, T_x=T_x, cache_len=len(kept), dtype=dtype)
+        plan = ccv3d.Plan(ccv3d.desc_for(conv))
+        x = rnd(1, T_x, H, W, Cin)
+        out, _ = plan.alloc_outputs("cuda")
+        buf = rnd(1, len(kept), H, W, Cin) if kept else None
+        head = plan.forward_qring(x, desc, codes, scales, head, buf, w, b, out)
+        torch.cuda.synchronize()
+        assert plan.status() == ccv3d.CCV3D_OK and plan.stats()["calls"] == 1
+        cache = np.stack(kept, 1) if kept else None
+        if kept:
+            assert np.array_equal(_np(buf), cache)
+        ref, _ = oracle.forward(oracle_params(conv), _np(x), cache, _np(w), _np(b))
+        assert_close(_np(out), ref, dtype)
+        kept = (kept + [quantise(_np(x)[:, t], fmt)[1] for t in range(T_x)])[-keep:]
+        # the new head finds them again
+        back = torch.empty(1, len(kept), H, W, Cin, dtype=x.dtype, device="cuda")
+        ccv3d.ccv3d_qcache_read(desc, codes, scales, head, len(kept), back)
+        assert np.array_equal(_np(back), np.stack(kept, 1))
+    assert ccv3d.ccv3d_block_get_status() == ccv3d.CCV3D_OK
+
+
+def _block_reference(x, p, fmt):
+    """The block on all frames x [T, H, W, C] in 64 bits: each convolution sees
+    its frame as it is and the two before it as the cache gives them back."""
+    T, H, W, C = x.shape
+
+    def act_norm(v, w):
+        u = norm(d(v).reshape(-1, v.shape[-1]), "rms", d(w), None, EPS)[0]
+        return (u * torch.sigmoid(u)).view(v.shape)
+
+    def conv(v, w, b):
+        out = []
+        held = [torch.from_numpy(quantise(_np(f), fmt)[1]).cuda() for f in v]
+        wt = d(w).permute(0, 4, 1, 2, 3)
+        for t in range(T):
+            frames = [held[t + k - 2] if t + k - 2 >= 0 else torch.zeros_like(held[0])
+                      for k in range(2)] + [d(v[t])]
+            z = torch.stack(frames).permute(3, 0, 1, 2)[None]
+            out.append(torch.nn.functional.conv3d(z, wt, d(b), padding=(0, 1, 1))[0, :, 0]
+                       .permute(1, 2, 0))
+        return torch.stack(out)
+
+    a = conv(act_norm(x, p["n1"]), p["w1"], p["b1"])
+    b = conv(act_norm(a, p["n2"]), p["w2"], p["b2"])
+    return b + d(x) @ d(p["ws"]).t() + d(p["bs"])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_residual_block_streamed(fmt):
+    T, H, W, C, Co = 5, 10, 18, 64, 96
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rnd = lambda *s, std=1.0, mean=0.0: (torch.randn(s, device="cuda", generator=g) * std
+                                         + mean).bfloat16()
+    p = dict(n1=rnd(C, mean=1.0, std=0.2), n2=rnd(Co, mean=1.0, std=0.2),
+             w1=rnd(Co, 3, 3, 3, C, std=(27 * C) ** -0.5), b1=rnd(Co, std=0.1),
+             w2=rnd(Co, 3, 3, 3, Co, std=(27 * Co) ** -0.5), b2=rnd(Co, std=0.1),
+             ws=rnd(Co, C, std=C ** -0.5), bs=rnd(Co, std=0.1))
+    x = rnd(T, H, W, C)
+    px = H * W
+    n1 = ccv3d.make_norm_desc(rows=px, C=C, act="silu", eps=EPS)
+    n2 = ccv3d.make_norm_desc(rows=px, C=Co, act="silu", eps=EPS)
+    sc = ccv3d.make_pointwise_desc(pixels=px, Cin=C, Cout=Co)
+    ws = ccv3d.alloc_workspace(ccv3d.ccv3d_pointwise_workspace(sc)[0])
+    q = [ccv3d.make_qcache_desc(N=1, H=H, W=W, C=c, ring_slots=3, format=fmt) for c in (C, Co)]
+    rings = [ccv3d.alloc_qcache(k) for k in q]
+    heads = [0, 0]
+    plans = {(i, l): ccv3d.Plan(ccv3d.make_desc(N=1, Cin=c, Cout=Co, H=H, W=W, T_x=1, cache_len=l))
+             for i, c in enumerate((C, Co)) for l in range(3)}
+    buf = torch.empty(2 * px * Co, dtype=torch.bfloat16, device="cuda")  # shared by both modules
+    y1, y2 = torch.empty(px, C, device="cuda").bfloat16(), torch.empty(px, Co, device="cuda").bfloat16()
+    a, b = (torch.empty(1, 1, H, W, Co, device="cuda").bfloat16() for _ in range(2))
+    out = torch.empty(T, H, W, Co, device="cuda").bfloat16()
+    for t in range(T):
+        l = min(t, 2)
+
+        def conv(i, v, w, bias, o):
+            c = (C, Co)[i]
+            scratch = buf[:l * px * c] if l else None
+            heads[i] = plans[i, l].forward_qring(v, q[i], *rings[i], heads[i], scratch, w, bias, o)
+
+        ccv3d.ccv3d_norm_forward(n1, x[t], None, None, None, None, p["n1"], None, None, y1)
+        conv(0, y1, p["w1"], p["b1"], a)
+        ccv3d.ccv3d_norm_forward(n2, a, None, None, None, None, p["n2"], None, None, y2)
+        conv(1, y2, p["w2"], p["b2"], b)
+        ccv3d.ccv3d_pointwise_forward(sc, x[t], p["ws"], p["bs"], b, out[t], None, ws)
+    torch.cuda.synchronize()
+    assert ccv3d.ccv3d_block_get_status() == ccv3d.CCV3D_OK
+    want = _block_reference(x, p, fmt)
+    # five bf16 roundings in a row (two norms, two convolutions, the sum), 2^-8
+    # each of values of the size of the output, and the codes that those
+    # roundings flip: a flipped code of the cache is a step of 2^-6 (int8, of
+    # the group's largest) or 2^-3 (e4m3, relative) in two of three taps, for
+    # the share of codes within 2^-8 of a border
+    step = {"int8": 2.0 ** -6, "e4m3": 2.0 ** -3}[fmt]
+    err = (d(out) - want).norm() / want.norm()
+    assert err <= 5 * 2.0 ** -8 + step * (2.0 ** -8 / step) ** 0.5
+    m = oracle.metrics(_np(out), _np(want))
+    assert m["nonfinite"] == 0
