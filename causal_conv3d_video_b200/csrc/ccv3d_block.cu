@@ -6,13 +6,17 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
+#include <mutex>
 
 #include "ccv3d.h"
 #include "elem.cuh"
 #include "norm.cuh"
 #include "pointwise_simt.cuh"
+#include "pointwise_tc.cuh"
 #include "qcache.cuh"
 
 using namespace ccv3d;
@@ -200,22 +204,228 @@ SumShape sum_shape(long long M, int N) {
     return s;
 }
 
-// Workspace of the backward pass, in this order: dP, column sums, partials.
-struct BwdWs {
-    size_t dp, sums, parts, total;
+// ---- tensor-core products
+// Shape of D(m, n) = sum over K on pw_tc_kernel.
+struct TcShape {
+    int BN, tiles_m, tiles_n, kblocks, splits, kb_per_split, stages, n_bufs, tmem_cols, ldp;
+    size_t smem, ws;
 };
-BwdWs backward_ws(const ccv3d_pointwise_desc* d) {
-    BwdWs w;
-    const size_t e = size_of(d->dtype);
-    w.dp = d->act != CCV3D_ACT_NONE ? pad256((size_t)d->pixels * d->Cout * e) : 0;
-    w.sums = pad256((size_t)sum_shape(d->pixels, d->Cout).chunks * d->Cout * 4);
-    w.parts = std::max(simt_ws(d->pixels, d->Cin, d->Cout), simt_ws(d->Cout, d->Cin, d->pixels));
-    w.total = w.dp + w.sums + w.parts;
+
+// Tile width and splits by the cost of the slowest pair, in SM cycles: a
+// 64-deep step of an M = 256 pair MMA of N = BN takes max(500, 2.64 BN) (four
+// instructions; measured on this GPU: about 3100 MAC a cycle and SM, and no
+// less than 125 cycles an instruction), a tile's epilogue about 12 BN beside
+// the next tile's steps, a split reduction's partials two trips at 3500
+// bytes a cycle and a launch of 4000.
+TcShape tc_shape(long long M, int N, long long K, bool b_mn, bool res, bool pre) {
+    TcShape s = {};
+    s.tiles_m = (int)up(M, kPtRows);
+    s.kblocks = (int)up(K, kPtK);
+    s.ldp = (int)up(N, 4) * 4;
+    double best = 1e300;
+    const int pairs = kSms / 2;
+    for (int bn = 32; bn <= 256; bn += 32) {
+        if (bn > 32 && bn - 32 >= N) break;
+        const int tn = (int)up(N, bn);
+        const long long tiles = (long long)s.tiles_m * tn;
+        for (int want = 1; want <= 128; want *= 2) {
+            const int per = (int)up(s.kblocks, want), splits = (int)up(s.kblocks, per);
+            if (want > 1 && (per < 4 || tiles * want / 2 >= pairs)) break;
+            const double step = std::max(500.0, 2.64 * bn), epi = 12.0 * bn;
+            const double waves = (double)up(tiles * splits, pairs);
+            double cost = waves * std::max(per * step, epi) + std::min(per * step, epi);
+            if (splits > 1) cost += 4000.0 + (double)splits * M * N * 8.0 / 3500.0;
+            if (cost < best * 0.999) {
+                best = cost;
+                s.BN = bn;
+                s.tiles_n = tn;
+                s.splits = splits;
+                s.kb_per_split = per;
+            }
+        }
+    }
+    const bool parts = s.splits > 1;
+    s.n_bufs = res && !parts ? 4 : 2;
+    s.stages = 10;
+    while (s.stages > 2 && pt_smem(b_mn, s.BN, s.stages, s.n_bufs, pre && !parts) > 227 * 1024)
+        --s.stages;
+    s.smem = pt_smem(b_mn, s.BN, s.stages, s.n_bufs, pre && !parts);
+    s.tmem_cols = 32;
+    while (s.tmem_cols < 2 * s.BN) s.tmem_cols *= 2;
+    s.ws = parts ? pad256((size_t)s.splits * M * s.ldp * 4) : 0;
+    return s;
+}
+
+// Bytes of an operand of `rows` rows copied to rows of a multiple of 8 (0:
+// its rows are that already).
+size_t pack_bytes(long long rows, int C) {
+    return C % 8 == 0 ? 0 : pad256((size_t)rows * up(C, 8) * 8 * 2);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    });
+    return fn;
+}
+
+// Map of a [rows][ld] bf16 matrix in boxes of `inner` x `outer` elements;
+// elements past `cols` (<= ld) of a row are read as 0 and not written.
+bool encode2d(CUtensorMap* m, const void* base, long long rows, int cols, int ld, int inner,
+              int outer) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)inner, (cuuint32_t)outer}, es[2] = {1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+                       strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+void set_tc_attrs() {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> done[kDevices];
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) {
+        cudaGetLastError();
+        return;
+    }
+    if (done[dev].load(std::memory_order_acquire)) return;
+    constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaFuncSetAttribute(pw_tc_kernel<false, false>, attr, 227 * 1024);
+    cudaFuncSetAttribute(pw_tc_kernel<false, true>, attr, 227 * 1024);
+    cudaFuncSetAttribute(pw_tc_kernel<true, true>, attr, 227 * 1024);
+    cudaGetLastError();
+    done[dev].store(true, std::memory_order_release);
+}
+
+const void* packed(const void* src, long long rows, int C, uint8_t*& at, cudaStream_t st) {
+    if (C % 8 == 0) return src;
+    const int Cp = (int)up(C, 8) * 8;
+    bf16* dst = reinterpret_cast<bf16*>(at);
+    at += pack_bytes(rows, C);
+    const long long n = rows * (Cp / 8);
+    pw_pack_kernel<<<(unsigned)std::min<long long>(up(n, 256), kSms * 16LL), 256, 0, st>>>(
+        static_cast<const bf16*>(src), dst, rows, C, Cp);
+    return dst;
+}
+
+// D = sum_k A B with the forward epilogue `o` (no bias, residual or pre for
+// gradients).  A: [M][K] rows of lda, or (A_MN) [K][M]; B likewise with N.
+template <bool A_MN, bool B_MN>
+ccv3d_status run_tc(const void* A, int lda, const void* B, int ldb, long long M, int N,
+                    long long K, const PwOut& o, float* partial, cudaStream_t st) {
+    if (encode_fn() == nullptr) return CCV3D_ERR_CUDA;
+    const TcShape s = tc_shape(M, N, K, B_MN, o.residual != nullptr, o.pre != nullptr);
+    PtParams p;
+    std::memset(&p, 0, sizeof(p));
+    const bool direct = N % 8 != 0;
+    bool ok = A_MN ? encode2d(&p.tm_a, A, K, (int)M, lda, 64, 64)
+                   : encode2d(&p.tm_a, A, M, (int)K, lda, 64, 128);
+    ok = ok && (B_MN ? encode2d(&p.tm_b, B, K, N, ldb, 64, 64)
+                     : encode2d(&p.tm_b, B, N, (int)K, ldb, 64, s.BN / 2));
+    const int ch = pt_chunk(s.BN);
+    if (s.splits > 1) {
+        p.partial = partial;
+    } else {
+        p.bias = static_cast<const bf16*>(o.bias);
+        p.residual = static_cast<const bf16*>(o.residual);
+        p.out = static_cast<bf16*>(o.out);
+        p.pre = static_cast<bf16*>(o.pre);
+        p.act = o.act;
+        p.direct = direct;
+        if (!direct) {
+            ok = ok && encode2d(&p.tm_out, o.out, M, N, N, ch, 32);
+            if (o.residual != nullptr) ok = ok && encode2d(&p.tm_res, o.residual, M, N, N, ch, 32);
+            if (o.pre != nullptr) ok = ok && encode2d(&p.tm_pre, o.pre, M, N, N, ch, 32);
+        }
+    }
+    if (!ok) return CCV3D_ERR_CUDA;
+    p.M = M;
+    p.N = N;
+    p.ldp = s.ldp;
+    p.tiles_m = s.tiles_m;
+    p.tiles_n = s.tiles_n;
+    p.BN = s.BN;
+    p.kblocks = s.kblocks;
+    p.splits = s.splits;
+    p.kb_per_split = s.kb_per_split;
+    p.stages = s.stages;
+    p.n_bufs = s.n_bufs;
+    p.tmem_cols = s.tmem_cols;
+    p.wait_limit_ns = kWaitLimitNs;
+    set_tc_attrs();
+    const long long total = (long long)s.tiles_m * s.tiles_n * s.splits;
+    if (total > 0x7fffffffLL / 8) return CCV3D_ERR_UNSUPPORTED;
+    const int grid = 2 * (int)std::min<long long>(total, kSms / 2);
+    pw_tc_kernel<A_MN, B_MN><<<grid, kPtThreads, s.smem, st>>>(p);
+    if (s.splits > 1) {
+        const long long blocks = std::min<long long>(up(M * N, 256), kSms * 16LL);
+        pw_join_kernel<bf16><<<(unsigned)blocks, 256, 0, st>>>(partial, s.splits, s.ldp, o);
+    }
+    return launched();
+}
+
+// Workspaces, in the order of their parts.  Forward: packed x and w, partials.
+struct FwdWs {
+    size_t packs, parts, total;
+};
+FwdWs forward_ws(const ccv3d_pointwise_desc* d) {
+    FwdWs w = {};
+    const long long M = d->pixels;
+    if (M <= kPwFewRows) return w;
+    if (d->dtype == CCV3D_FP32) {
+        w.parts = simt_ws(M, d->Cout, d->Cin);
+    } else {
+        w.packs = pack_bytes(M, d->Cin) + pack_bytes(d->Cout, d->Cin);
+        // (a residual or pre changes the buffers, not the splits)
+        w.parts = tc_shape(M, d->Cout, d->Cin, false, false, false).ws;
+    }
+    w.total = w.packs + w.parts;
     return w;
 }
 
-// D = A B^T on FFMA with the forward epilogue (o.out of type T).
-template <typename T, bool AK, bool BK>
+// Backward: dP, column sums, packed x and w, partials (of dx, then of dw).
+struct BwdWs {
+    size_t dp, sums, packs, parts, total;
+};
+bool makes_dp(const ccv3d_pointwise_desc* d) {
+    return d->act != CCV3D_ACT_NONE || (d->dtype == CCV3D_BF16 && d->Cout % 8 != 0);
+}
+// Elements of a row of dP.
+int dp_row(const ccv3d_pointwise_desc* d) {
+    return d->dtype == CCV3D_BF16 ? (int)up(d->Cout, 8) * 8 : d->Cout;
+}
+BwdWs backward_ws(const ccv3d_pointwise_desc* d) {
+    BwdWs w = {};
+    const long long M = d->pixels;
+    w.dp = makes_dp(d) ? pad256((size_t)M * dp_row(d) * size_of(d->dtype)) : 0;
+    w.sums = pad256((size_t)sum_shape(M, d->Cout).chunks * d->Cout * 4);
+    if (d->dtype == CCV3D_FP32) {
+        w.parts = std::max(simt_ws(M, d->Cin, d->Cout), simt_ws(d->Cout, d->Cin, M));
+    } else {
+        w.packs = pack_bytes(M, d->Cin) + pack_bytes(d->Cout, d->Cin);
+        w.parts = std::max(tc_shape(M, d->Cin, d->Cout, true, false, false).ws,
+                           tc_shape(d->Cout, d->Cin, M, true, false, false).ws);
+    }
+    w.total = w.dp + w.sums + w.packs + w.parts;
+    return w;
+}
+
+// D = A B^T on FFMA, fp32.
+template <bool AK, bool BK>
 ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb, long long M,
                       int N, long long K, PwOut o, float* partial, cudaStream_t st) {
     PwSimt p;
@@ -228,8 +438,7 @@ ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb
     p.M = M;
     p.N = N;
     p.K = K;
-    const int per16 = 16 / (int)sizeof(T);
-    p.vec = lda % per16 == 0 && ldb % per16 == 0;
+    p.vec = lda % 4 == 0 && ldb % 4 == 0;
     p.splits = simt_splits(M, N, K);
     p.k_per_split = up(up(K, p.splits), kPwK) * kPwK;
     p.splits = (int)std::max<long long>(1, up(K, p.k_per_split));
@@ -237,10 +446,10 @@ ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb
     p.o.partial = p.splits > 1 ? partial : nullptr;
     const long long tiles = up(M, kPwTile) * up(N, kPwTile);
     if (tiles > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;
-    pw_simt_kernel<T, AK, BK><<<dim3((unsigned)tiles, 1, p.splits), 256, 0, st>>>(p);
+    pw_simt_kernel<float, AK, BK><<<dim3((unsigned)tiles, 1, p.splits), 256, 0, st>>>(p);
     if (p.splits > 1) {
         const long long blocks = std::min<long long>(up(M * N, 256), kSms * 16LL);
-        pw_join_kernel<T><<<(unsigned)blocks, 256, 0, st>>>(partial, p.splits, o);
+        pw_join_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(partial, p.splits, N, o);
     }
     return launched();
 }
@@ -262,8 +471,17 @@ ccv3d_status forward_type(const ccv3d_pointwise_desc* d, const void* x, const vo
         else run_rows<T, 8, 4>(xt, wt, d->Cin, o, st);
         return launched();
     }
-    return run_simt<T, true, true>(x, w, d->Cin, d->Cin, d->pixels, d->Cout, d->Cin, o,
-                                   static_cast<float*>(ws), st);
+    if constexpr (sizeof(T) == 4) {
+        return run_simt<true, true>(x, w, d->Cin, d->Cin, d->pixels, d->Cout, d->Cin, o,
+                                    static_cast<float*>(ws), st);
+    } else {
+        uint8_t* at = static_cast<uint8_t*>(ws);
+        const void* A = packed(x, d->pixels, d->Cin, at, st);
+        const void* B = packed(w, d->Cout, d->Cin, at, st);
+        const int ld = (int)up(d->Cin, 8) * 8;
+        return run_tc<false, false>(A, ld, B, ld, d->pixels, d->Cout, d->Cin, o,
+                                    reinterpret_cast<float*>(at), st);
+    }
 }
 
 template <typename T>
@@ -271,13 +489,14 @@ ccv3d_status backward_type(const ccv3d_pointwise_desc* d, const void* x, const v
                            const void* pre, const void* dout, void* dx, void* dw, void* dbias,
                            void* ws, cudaStream_t st) {
     const long long M = d->pixels;
-    const int K = d->Cin, N = d->Cout;
+    const int K = d->Cin, N = d->Cout, ldp = dp_row(d);
     const BwdWs b = backward_ws(d);
     uint8_t* at = static_cast<uint8_t*>(ws);
     T* dp = reinterpret_cast<T*>(at);
     float* sums = reinterpret_cast<float*>(at + b.dp);
-    float* parts = reinterpret_cast<float*>(at + b.dp + b.sums);
-    const bool make = d->act != CCV3D_ACT_NONE && (dx != nullptr || dw != nullptr);
+    uint8_t* packs = at + b.dp + b.sums;
+    float* parts = reinterpret_cast<float*>(packs + b.packs);
+    const bool make = makes_dp(d) && (dx != nullptr || dw != nullptr);
     if (make || dbias != nullptr) {
         const SumShape s = sum_shape(M, N);
         const dim3 grid(s.col_blocks, (unsigned)s.chunks);
@@ -286,11 +505,11 @@ ccv3d_status backward_type(const ccv3d_pointwise_desc* d, const void* x, const v
         float* cs = dbias != nullptr ? sums : nullptr;
         T* tdp = make ? dp : nullptr;
         if (N % 8 == 0)
-            pw_dact_kernel<T, true><<<grid, 256, 0, st>>>(tp, td, tdp, cs, M, N, N, d->act, s.tpr,
-                                                         s.chunk);
+            pw_dact_kernel<T, true><<<grid, 256, 0, st>>>(tp, td, tdp, cs, M, N, ldp, d->act,
+                                                         s.tpr, s.chunk);
         else
-            pw_dact_kernel<T, false><<<grid, 256, 0, st>>>(tp, td, tdp, cs, M, N, N, d->act, s.tpr,
-                                                          s.chunk);
+            pw_dact_kernel<T, false><<<grid, 256, 0, st>>>(tp, td, tdp, cs, M, N, ldp, d->act,
+                                                          s.tpr, s.chunk);
         if (dbias != nullptr)
             pw_colsum_kernel<T><<<(unsigned)up(N, 32), dim3(32, 32), 0, st>>>(
                 sums, (int)s.chunks, N, static_cast<T*>(dbias));
@@ -304,13 +523,23 @@ ccv3d_status backward_type(const ccv3d_pointwise_desc* d, const void* x, const v
         o.out = dx;
         o.M = M;
         o.N = K;
-        r = run_simt<T, true, false>(dP, w, N, K, M, K, N, o, parts, st);
+        if constexpr (sizeof(T) == 4) {
+            r = run_simt<true, false>(dP, w, N, K, M, K, N, o, parts, st);
+        } else {
+            const void* B = packed(w, N, K, packs, st);
+            r = run_tc<false, true>(dP, ldp, B, (int)up(K, 8) * 8, M, K, N, o, parts, st);
+        }
     }
     if (r == CCV3D_OK && dw != nullptr) {
         o.out = dw;
         o.M = N;
         o.N = K;
-        r = run_simt<T, false, false>(dP, x, N, K, N, K, M, o, parts, st);
+        if constexpr (sizeof(T) == 4) {
+            r = run_simt<false, false>(dP, x, N, K, N, K, M, o, parts, st);
+        } else {
+            const void* B = packed(x, M, K, packs, st);
+            r = run_tc<true, true>(dP, ldp, B, (int)up(K, 8) * 8, N, K, M, o, parts, st);
+        }
     }
     return r;
 }
@@ -483,7 +712,7 @@ ccv3d_status ccv3d_pointwise_workspace(const ccv3d_pointwise_desc* d, size_t* fo
     if (c != CCV3D_OK) return c;
     if (d->pixels == 0) return CCV3D_OK;
     if (forward_bytes)
-        *forward_bytes = d->pixels <= kPwFewRows ? 0 : simt_ws(d->pixels, d->Cout, d->Cin);
+        *forward_bytes = forward_ws(d).total;
     if (backward_bytes) *backward_bytes = backward_ws(d).total;
     return CCV3D_OK;
 }

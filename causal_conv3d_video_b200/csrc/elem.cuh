@@ -10,6 +10,8 @@
 
 namespace ccv3d {
 
+typedef __nv_bfloat16 bf16_t;
+
 // First error recorded on this device by a kernel of ccv3d_norm_*,
 // ccv3d_pointwise_* or ccv3d_qcache_* (0: none): a bounded wait that ran out,
 // or a bounds violation of the checked build.

@@ -139,13 +139,15 @@ __global__ void __launch_bounds__(256) pw_simt_kernel(const __grid_constant__ Pw
 
 // The partials of a split reduction, added in order, through the epilogue.
 template <typename T>
-__global__ void __launch_bounds__(256) pw_join_kernel(const float* partial, int splits,
+__global__ void __launch_bounds__(256) pw_join_kernel(const float* partial, int splits, int ldp,
                                                       const __grid_constant__ PwOut o) {
     const long long total = o.M * o.N, step = (long long)gridDim.x * blockDim.x;
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
+        const long long m = i / o.N;
+        const int n = (int)(i - m * o.N);
         float u = 0.0f;
-        for (int s = 0; s < splits; ++s) u += partial[s * total + i];
-        pw_store<T>(o, i / o.N, (int)(i % o.N), u);
+        for (int s = 0; s < splits; ++s) u += partial[(s * o.M + m) * ldp + n];
+        pw_store<T>(o, m, n, u);
     }
 }
 
