@@ -207,7 +207,8 @@ SumShape sum_shape(long long M, int N) {
 // ---- tensor-core products
 // Shape of D(m, n) = sum over K on pw_tc_kernel.
 struct TcShape {
-    int BN, tiles_m, tiles_n, kblocks, splits, kb_per_split, stages, n_bufs, tmem_cols, ldp;
+    int BN, tiles_m, tiles_n, kblocks, splits, kb_per_split, stages, chunk, n_bufs, n_pres, res_bufs,
+        tmem_cols, ldp;
     size_t smem, ws;
 };
 
@@ -245,11 +246,17 @@ TcShape tc_shape(long long M, int N, long long K, bool b_mn, bool res, bool pre)
         }
     }
     const bool parts = s.splits > 1;
-    s.n_bufs = res && !parts ? 4 : 2;
+    // staging: two buffers in turn a warp, for out and for pre; with pre and a
+    // residual 32-column chunks, so that four operand stages are left
+    s.chunk = s.BN % 64 != 0 || (res && pre) ? 32 : 64;
+    s.n_bufs = parts ? 0 : 2;
+    s.n_pres = parts || !pre ? 0 : 2;
+    s.res_bufs = parts || !res || N % 8 != 0 ? 0 : kPtResBufs;
     s.stages = 10;
-    while (s.stages > 2 && pt_smem(b_mn, s.BN, s.stages, s.n_bufs, pre && !parts) > 227 * 1024)
+    while (s.stages > 2 &&
+           pt_smem(b_mn, s.BN, s.stages, s.chunk, s.n_bufs + s.n_pres, s.res_bufs) > 227 * 1024)
         --s.stages;
-    s.smem = pt_smem(b_mn, s.BN, s.stages, s.n_bufs, pre && !parts);
+    s.smem = pt_smem(b_mn, s.BN, s.stages, s.chunk, s.n_bufs + s.n_pres, s.res_bufs);
     s.tmem_cols = 32;
     while (s.tmem_cols < 2 * s.BN) s.tmem_cols *= 2;
     s.ws = parts ? pad256((size_t)s.splits * M * s.ldp * 4) : 0;
@@ -336,7 +343,7 @@ ccv3d_status run_tc(const void* A, int lda, const void* B, int ldb, long long M,
                    : encode2d(&p.tm_a, A, M, (int)K, lda, 64, 128);
     ok = ok && (B_MN ? encode2d(&p.tm_b, B, K, N, ldb, 64, 64)
                      : encode2d(&p.tm_b, B, N, (int)K, ldb, 64, s.BN / 2));
-    const int ch = pt_chunk(s.BN);
+    const int ch = s.chunk;
     if (s.splits > 1) {
         p.partial = partial;
     } else {
@@ -348,7 +355,7 @@ ccv3d_status run_tc(const void* A, int lda, const void* B, int ldb, long long M,
         p.direct = direct;
         if (!direct) {
             ok = ok && encode2d(&p.tm_out, o.out, M, N, N, ch, 32);
-            if (o.residual != nullptr) ok = ok && encode2d(&p.tm_res, o.residual, M, N, N, ch, 32);
+            if (o.residual != nullptr) ok = ok && encode2d(&p.tm_res, o.residual, M, N, N, ch, 128);
             if (o.pre != nullptr) ok = ok && encode2d(&p.tm_pre, o.pre, M, N, N, ch, 32);
         }
     }
@@ -363,13 +370,19 @@ ccv3d_status run_tc(const void* A, int lda, const void* B, int ldb, long long M,
     p.splits = s.splits;
     p.kb_per_split = s.kb_per_split;
     p.stages = s.stages;
+    p.chunk = s.chunk;
     p.n_bufs = s.n_bufs;
+    p.n_pres = s.n_pres;
+    p.res_bufs = s.res_bufs;
     p.tmem_cols = s.tmem_cols;
     p.wait_limit_ns = kWaitLimitNs;
     set_tc_attrs();
     const long long total = (long long)s.tiles_m * s.tiles_n * s.splits;
     if (total > 0x7fffffffLL / 8) return CCV3D_ERR_UNSUPPORTED;
-    const int grid = 2 * (int)std::min<long long>(total, kSms / 2);
+    const int pairs = (int)std::min<long long>(total, kSms / 2), grid = 2 * pairs;
+    p.step_n = pairs % s.tiles_n;
+    p.step_m = pairs / s.tiles_n % s.tiles_m;
+    p.step_s = pairs / s.tiles_n / s.tiles_m;
     pw_tc_kernel<A_MN, B_MN><<<grid, kPtThreads, s.smem, st>>>(p);
     if (s.splits > 1) {
         const long long blocks = std::min<long long>(up(M * N, 256), kSms * 16LL);

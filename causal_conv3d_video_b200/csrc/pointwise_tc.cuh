@@ -16,11 +16,15 @@
 // of A in L2.  Long reductions over few tiles (dw, few rows) are split; the
 // fp32 partials are joined, in order, by a second launch.
 //
-// Epilogue: each of four warps owns 32 rows of the CTA's 128 and works alone,
-// 64 (or 32) columns at a time: TMEM -> registers, + bias, activation,
-// + residual, one rounding to bf16, into a swizzled shared-memory buffer, TMA
-// store.  The residual chunk was loaded by TMA into that same buffer up to
-// two chunks ahead.
+// Epilogue: eight warps, two for each 32 of the CTA's 128 rows, each on its
+// own, 64 (or 32) columns at a time, the two taking turns: TMEM -> registers,
+// + bias, activation, + residual, one rounding to bf16, into a swizzled
+// shared-memory buffer, TMA store.  One more warp runs ahead of them with the
+// residual (TMA, a ring of chunks of all 128 rows) and the tiles' bias, so that
+// no global-memory latency is left in a chunk: with each warp fetching its own
+// residual and bias, a chunk took 2500 cycles, most of them waiting.  A chunk's
+// shared-memory reads are all issued before its writes: interleaved, the bias
+// reads alone waited 1750 cycles.
 #pragma once
 #include "elem.cuh"
 #include "epilogue.cuh"
@@ -30,7 +34,11 @@
 
 namespace ccv3d {
 
-constexpr int kPtThreads = 192;  // warp 0: loads, warp 1: MMAs, warps 2-5: epilogue
+constexpr int kPtEpiWarps = 8;
+// warp 0: operand loads, 1: MMAs, 2: residual and bias, 4-11: the epilogue
+// (a warp reads the TMEM lanes of its number modulo 4)
+constexpr int kPtThreads = 128 + 32 * kPtEpiWarps;
+constexpr int kPtResBufs = 4;    // chunks of the residual's ring
 constexpr int kPtRows = 256;     // rows of a pair's tile
 constexpr int kPtK = 64;
 constexpr int kPtA = 128 * kPtK * 2;     // bytes of A a CTA and stage
@@ -44,7 +52,11 @@ struct PtParams {
     float* partial;          // not NULL: fp32 partials [split][M][ldp] only
     long long M;
     int N, ldp, act, direct;
-    int tiles_m, tiles_n, BN, kblocks, splits, kb_per_split, stages, n_bufs, tmem_cols;
+    int tiles_m, tiles_n, BN, kblocks, splits, kb_per_split, stages, tmem_cols;
+    int chunk;               // columns the epilogue moves at a time: 64 or 32
+    int n_bufs, n_pres;      // staging buffers of an epilogue warp
+    int res_bufs;            // kPtResBufs, or 0 without a ring
+    int step_n, step_m, step_s;  // number of pairs, in tiles of the walk
     uint64_t wait_limit_ns;
 };
 
@@ -88,106 +100,162 @@ __device__ __forceinline__ uint64_t pt_desc_mn(uint32_t saddr) {
 __host__ __device__ constexpr int pt_b_bytes(bool mn, int bn) {
     return mn ? ((bn / 2 + 63) / 64) * kPtBox : (bn / 2) * kPtK * 2;
 }
-__host__ __device__ constexpr int pt_chunk(int bn) { return bn % 64 == 0 ? 64 : 32; }
-__host__ __device__ constexpr size_t pt_smem(bool b_mn, int bn, int stages, int n_bufs, bool pre) {
+__host__ __device__ constexpr size_t pt_smem(bool b_mn, int bn, int stages, int chunk,
+                                             int bufs, int res_bufs) {
     return 1024 + (size_t)stages * (kPtA + pt_b_bytes(b_mn, bn)) +
-           (size_t)4 * 32 * pt_chunk(bn) * 2 * (n_bufs + (pre ? 2 : 0)) + (size_t)bn * 4 +
-           (size_t)(2 * stages + 4 + 16) * 8 + 16;
+           (size_t)chunk * 2 * (kPtEpiWarps * 32 * bufs + 128 * res_bufs) +
+           (size_t)bn * 4 * 2 + (size_t)(2 * stages + 8 + 2 * kPtResBufs) * 8 + 16;
 }
 
-struct PtItem {
-    int m, n, split, kb0, kb1;  // tile of 256 rows, tile of BN columns
-};
-__device__ __forceinline__ PtItem pt_item(const PtParams& p, int i) {
-    PtItem t;
-    t.n = i % p.tiles_n;
-    i /= p.tiles_n;
-    t.m = i % p.tiles_m;
-    t.split = i / p.tiles_m;
-    t.kb0 = t.split * p.kb_per_split;
-    t.kb1 = min(t.kb0 + p.kb_per_split, p.kblocks);
-    return t;
-}
-
-// One chunk of kCh columns of a warp's 32 rows (lane = row): registers u from
-// TMEM, then everything up to the store.
-template <int kCh>
-__device__ __forceinline__ void pt_epilogue(const PtParams& p, uint32_t tacc, int pair, int G,
-                                            int total, uint32_t rank, bool leader, int warp,
-                                            int lane, uint8_t* staging, float* bias_s,
-                                            uint64_t* acc_full, uint64_t* acc_empty,
-                                            uint64_t* res_bar) {
-    constexpr int kRowB = kCh * 2, kBuf = 32 * kRowB;
-    const int q = warp & 3, etid = threadIdx.x - 64;
-    const int nb = p.n_bufs, nch = p.BN / kCh;
-    uint8_t* bufs = staging + (size_t)q * kBuf * nb;
-    uint8_t* pres = staging + (size_t)4 * kBuf * nb + (size_t)q * kBuf * 2;
-    uint64_t* bars = res_bar + q * 4;  // one per residual buffer
-    const uint32_t empty_leader = pt_mapa(smem_u32(acc_empty), 0);
-    const bool res_tma = p.residual != nullptr && !p.direct && p.partial == nullptr;
-    const int items = (total - pair + G - 1) / G;  // of this pair
-    const int chunks = items * nch;
-    // chunk j of this warp: whether it lies in D at all, and where
-    auto place = [&](int j, int& r0, int& c0) {
-        const PtItem t = pt_item(p, pair + (j / nch) * G);
-        const long long r = (long long)t.m * kPtRows + rank * 128 + q * 32;
-        r0 = (int)r;  // M < 2^31 - 256
-        c0 = t.n * p.BN + (j % nch) * kCh;
-        return r < p.M && c0 < p.N;
-    };
-    auto fetch = [&](int j) {  // lane 0: residual chunk j into its buffer
-        int r0, c0;
-        if (j >= chunks || !place(j, r0, c0)) return;
-        const uint32_t bar = smem_u32(&bars[j & 3]);
-        mbar_arrive_expect_tx(bar, kBuf);
-        pt_load(smem_u32(bufs + (j & 3) * kBuf), &p.tm_res, bar, c0, r0);
-    };
-    uint32_t phases = 0;  // parity of each residual buffer's next completion
-    if (res_tma && lane == 0) {
-        fetch(0);
-        fetch(1);
+// A role's walk over its pair's work items: item i = (split, m, n), n fastest,
+// i = pair, pair + G, ...; the step G is split into the three counters once on
+// the host, so that a step is additions with carries.
+struct PtWalk {
+    int n, m, split, it, left;
+    __device__ __forceinline__ PtWalk(const PtParams& p, int pair, int G) {
+        const int total = p.tiles_m * p.tiles_n * p.splits;
+        n = pair % p.tiles_n;
+        const int r = pair / p.tiles_n;
+        m = r % p.tiles_m;
+        split = r / p.tiles_m;
+        it = 0;
+        left = (total - pair + G - 1) / G;
     }
+    __device__ __forceinline__ void next(const PtParams& p) {
+        n += p.step_n;
+        m += p.step_m;
+        split += p.step_s;
+        if (n >= p.tiles_n) {
+            n -= p.tiles_n;
+            ++m;
+        }
+        if (m >= p.tiles_m) {
+            m -= p.tiles_m;
+            ++split;
+        }
+        ++it;
+        --left;
+    }
+    __device__ __forceinline__ int kb0(const PtParams& p) const { return split * p.kb_per_split; }
+    __device__ __forceinline__ int kb1(const PtParams& p) const {
+        return min(kb0(p) + p.kb_per_split, p.kblocks);
+    }
+};
+
+struct PtShared {
+    uint8_t* staging;     // [epilogue warps][n_bufs + n_pres][32 rows][chunk]
+    uint8_t* res;         // [res_bufs][128 rows][chunk]
+    float* bias;          // [2][BN]
+    uint64_t *acc_full, *acc_empty, *bias_full, *bias_empty, *res_full, *res_empty;
+};
+
+// The warp that runs ahead of the epilogue: the bias of each tile (two tiles)
+// and its residual chunks (res_bufs chunks).
+template <int kCh>
+__device__ __forceinline__ void pt_ahead(const PtParams& p, const PtShared& sh, int pair, int G,
+                                         uint32_t rank, int lane) {
+    constexpr uint32_t kBytes = 128 * kCh * 2;
+    if (p.partial != nullptr) return;
+    const int nch = p.BN / kCh;
+    Ring ring;
+    int issued = 0;
     bool ok = true;
-    int bias_tile = -1;
-    for (int it = 0, j = 0; it < items; ++it) {
-        const PtItem t = pt_item(p, pair + it * G);
-        const int b = it & 1;
-        if (ok && !mbar_wait(smem_u32(&acc_full[b]), (uint32_t)((it >> 1) & 1), &g_block_status,
-                             p.wait_limit_ns))
+    for (PtWalk w(p, pair, G); w.left > 0; w.next(p)) {
+        if (p.bias != nullptr) {
+            const int b = w.it & 1;
+            if (w.it >= 2 && !mbar_wait(smem_u32(&sh.bias_empty[b]), (uint32_t)(((w.it >> 1) & 1) ^ 1),
+                                        &g_block_status, p.wait_limit_ns))
+                ok = false;
+            for (int i = lane; i < p.BN; i += 32) {
+                const int c = w.n * p.BN + i;
+                sh.bias[b * p.BN + i] = c < p.N ? (float)p.bias[c] : 0.0f;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.bias_full[b]));
+        }
+        if (p.res_bufs > 0 && lane == 0) {
+            const int r0 = w.m * kPtRows + (int)rank * 128;
+            for (int c = 0; c < nch; ++c, ++issued) {
+                const uint32_t bar = smem_u32(&sh.res_full[ring.st]);
+                if (issued >= p.res_bufs && !mbar_wait(smem_u32(&sh.res_empty[ring.st]), ring.ph ^ 1u,
+                                                       &g_block_status, p.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                // (a box outside the matrix is zeros)
+                mbar_arrive_expect_tx(bar, kBytes);
+                pt_load(smem_u32(sh.res + ring.st * kBytes), &p.tm_res, bar,
+                        w.n * p.BN + c * kCh, r0);
+                ring.next(p.res_bufs);
+            }
+        }
+        if (__any_sync(0xffffffffu, !ok)) return;
+    }
+}
+
+// The epilogue of one warp: every second chunk of kCh columns of its 32 rows.
+template <int kCh>
+__device__ __forceinline__ void pt_epilogue(const PtParams& p, const PtShared& sh, uint32_t tmem,
+                                            int pair, int G, uint32_t rank, bool leader, int warp,
+                                            int lane) {
+    constexpr int kRowB = kCh * 2, kBuf = 32 * kRowB;
+    const int q = warp & 3, wid = warp - 4, set = wid >> 2;
+    const int nch = p.BN / kCh;
+    uint8_t* bufs = sh.staging + (size_t)wid * kBuf * (p.n_bufs + p.n_pres);
+    uint8_t* pres = bufs + (size_t)p.n_bufs * kBuf;
+    const uint32_t empty_leader = pt_mapa(smem_u32(sh.acc_empty), 0);
+    const bool whole = p.partial == nullptr, biased = whole && p.bias != nullptr;
+    int turn = 0;  // staging buffer
+    int first = 0;  // chunks of the tiles before this one
+    bool ok = true;
+    for (PtWalk w(p, pair, G); w.left > 0; w.next(p), first += nch) {
+        const int b = w.it & 1;
+        const uint32_t round = (uint32_t)((w.it >> 1) & 1);
+        const int r0 = w.m * kPtRows + (int)rank * 128 + q * 32;  // M < 2^31 - 256
+        const int c_set = (set + first) & 1;
+        if (biased && ok && !mbar_wait(smem_u32(&sh.bias_full[b]), round, &g_block_status,
+                                       p.wait_limit_ns))
+            ok = false;
+        if (ok && !mbar_wait(smem_u32(&sh.acc_full[b]), round, &g_block_status, p.wait_limit_ns))
             ok = false;
         tc_fence_after();
-        if (t.n != bias_tile && p.partial == nullptr) {  // (uniform over the four warps)
-            epi_bar();
-            for (int i = etid; i < p.BN; i += 128) {
-                const int c = t.n * p.BN + i;
-                bias_s[i] = p.bias != nullptr && c < p.N ? (float)p.bias[c] : 0.0f;
+        const uint32_t tacc = tmem + (uint32_t)(b * p.BN) + ((uint32_t)(q * 32) << 16);
+        const float* bias = sh.bias + b * p.BN;
+        auto drained = [&]() {  // this warp has read the accumulator (and the bias)
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(smem_u32(&sh.acc_empty[b]));
+                else pt_arrive_remote(empty_leader + (uint32_t)(b * 8));
+                if (biased) mbar_arrive(smem_u32(&sh.bias_empty[b]));
             }
-            epi_bar();
-            bias_tile = t.n;
-        }
-        for (int c = 0; c < nch; ++c, ++j) {
-            int r0, c0;
-            const bool inside = place(j, r0, c0);
+        };
+        if (c_set >= nch) drained();
+        for (int c = c_set; c < nch; c += 2) {
+            const int c0 = w.n * p.BN + c * kCh;
+            const bool in = r0 < p.M && c0 < p.N;
             uint32_t v[kCh];
             __syncwarp();  // lanes left a wait or lane 0's stores: the load wants them together
 #pragma unroll
             for (int i = 0; i < kCh / 16; ++i)
-                tmem_ld_32x32b_x16(tacc + (uint32_t)(b * p.BN) + ((uint32_t)(q * 32) << 16) +
-                                       (uint32_t)(c * kCh + i * 16),
+                tmem_ld_32x32b_x16(tacc + (uint32_t)(c * kCh + i * 16),
                                    *reinterpret_cast<uint32_t(*)[16]>(&v[i * 16]));
             tmem_ld_wait();
-            if (c == nch - 1) {  // this accumulator is drained: back to the MMAs
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (leader) mbar_arrive(smem_u32(&acc_empty[b]));
-                    else pt_arrive_remote(empty_leader + (uint32_t)(b * 8));
+            if (biased) {
+#pragma unroll
+                for (int i = 0; i < kCh; i += 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(bias + c * kCh + i);
+                    v[i] = __float_as_uint(__uint_as_float(v[i]) + t.x);
+                    v[i + 1] = __float_as_uint(__uint_as_float(v[i + 1]) + t.y);
+                    v[i + 2] = __float_as_uint(__uint_as_float(v[i + 2]) + t.z);
+                    v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) + t.w);
                 }
             }
-            if (p.partial != nullptr) {
-                const long long row = (long long)r0 + lane;
-                if (inside && ok && row < p.M) {
-                    float* dst = p.partial + ((long long)t.split * p.M + row) * p.ldp + c0;
+            if (c + 2 >= nch) drained();
+            if (!whole) {
+                const long long r = (long long)r0 + lane;
+                if (in && ok && r < p.M) {
+                    float* dst = p.partial + ((long long)w.split * p.M + r) * p.ldp + c0;
 #pragma unroll
                     for (int i = 0; i < kCh; i += 4)
                         if (c0 + i < p.ldp &&
@@ -198,80 +266,106 @@ __device__ __forceinline__ void pt_epilogue(const PtParams& p, uint32_t tacc, in
                 }
                 continue;
             }
-            // buffers: all but the last chunk's store have been read
-            if (lane == 0) {
-                bulk_wait_group_read1();
-                if (res_tma) fetch(j + 2);
-            }
+            // the store before the last one has been read: its buffer is free
+            if (lane == 0) bulk_wait_group_read1();
             __syncwarp();
-            uint8_t* buf = bufs + (nb == 4 ? (j & 3) : (j & 1)) * kBuf;
-            uint8_t* row_b = buf + lane * kRowB;
-            if (res_tma && inside) {
-                const int k = j & 3;
-                if (ok && !mbar_wait(smem_u32(&bars[k]), (phases >> k) & 1u, &g_block_status,
-                                     p.wait_limit_ns))
-                    ok = false;
-                phases ^= 1u << k;
-            } else if (p.residual != nullptr && p.direct) {
-                // row by row, lanes along the columns
-                for (int r = 0; r < 32; ++r)
+            uint8_t* buf = bufs + turn * kBuf;
+            uint8_t* pre = pres + turn * kBuf;
+            if (p.pre != nullptr) {
 #pragma unroll
-                    for (int i = lane; i < kCh; i += 32) {
-                        const long long row = (long long)r0 + r;
-                        const bf16_t x = inside && row < p.M && c0 + i < p.N
-                                             ? p.residual[row * p.N + c0 + i] : bf16_t(0.0f);
-                        *reinterpret_cast<bf16_t*>(buf + r * kRowB +
-                                                   (swizzled_chunk<kRowB>(i >> 3, r) << 4) +
-                                                   (i & 7) * 2) = x;
-                    }
-                __syncwarp();
+                for (int i = 0; i < kCh / 8; ++i) {
+                    float t[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) t[k] = __uint_as_float(v[i * 8 + k]);
+                    *reinterpret_cast<uint4*>(pre + lane * kRowB +
+                                              (swizzled_chunk<kRowB>(i, lane) << 4)) =
+                        pack8<bf16_t, true>(t).a;
+                }
             }
-            uint8_t* row_p = pres + (j & 1) * kBuf + lane * kRowB;
+            if (p.act == kActSilu) {
+#pragma unroll
+                for (int i = 0; i < kCh; ++i)
+                    v[i] = __float_as_uint(act_of<bf16_t>(__uint_as_float(v[i]), kActSilu));
+            } else if (p.act == kActGelu) {
+#pragma unroll
+                for (int i = 0; i < kCh; ++i)
+                    v[i] = __float_as_uint(act_of<bf16_t>(__uint_as_float(v[i]), kActGelu));
+            }
+            if (p.residual != nullptr) {
+                const uint8_t* src = buf;
+                const int j = first + c, slot = j % kPtResBufs;
+                if (p.res_bufs > 0) {
+                    if (ok && !mbar_wait(smem_u32(&sh.res_full[slot]),
+                                         (uint32_t)((j / kPtResBufs) & 1), &g_block_status,
+                                         p.wait_limit_ns))
+                        ok = false;
+                    src = sh.res + (size_t)(slot * 4 + q) * kBuf;
+                } else {  // row by row, lanes along the columns
+                    for (int r = 0; r < 32; ++r)
+#pragma unroll
+                        for (int i = lane; i < kCh; i += 32) {
+                            const long long at = (long long)r0 + r;
+                            *reinterpret_cast<bf16_t*>(buf + r * kRowB +
+                                                       (swizzled_chunk<kRowB>(i >> 3, r) << 4) +
+                                                       (i & 7) * 2) =
+                                in && at < p.M && c0 + i < p.N ? p.residual[at * p.N + c0 + i]
+                                                               : bf16_t(0.0f);
+                        }
+                    __syncwarp();
+                }
+                Raw8<bf16_t, true> res[kCh / 8];
+#pragma unroll
+                for (int i = 0; i < kCh / 8; ++i)
+                    res[i].a = *reinterpret_cast<const uint4*>(
+                        src + lane * kRowB + (swizzled_chunk<kRowB>(i, lane) << 4));
+#pragma unroll
+                for (int i = 0; i < kCh / 8; ++i) {
+                    float t[8];
+                    unpack8<bf16_t, true>(res[i], t);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[i * 8 + k] = __float_as_uint(__uint_as_float(v[i * 8 + k]) + t[k]);
+                }
+                if (p.res_bufs > 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.res_empty[slot]));
+                }
+            }
 #pragma unroll
             for (int i = 0; i < kCh / 8; ++i) {
-                float u[8];
+                float t[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    u[k] = __uint_as_float(v[i * 8 + k]) + bias_s[c * kCh + i * 8 + k];
-                const int at = swizzled_chunk<kRowB>(i, lane) << 4;
-                if (p.pre != nullptr)
-                    *reinterpret_cast<uint4*>(row_p + at) = pack8<bf16_t, true>(u).a;
-                if (p.act != kActNone)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) u[k] = act_of<bf16_t>(u[k], p.act);
-                if (p.residual != nullptr) {
-                    Raw8<bf16_t, true> r;
-                    r.a = *reinterpret_cast<const uint4*>(row_b + at);
-                    float f[8];
-                    unpack8<bf16_t, true>(r, f);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) u[k] += f[k];
-                }
-                *reinterpret_cast<uint4*>(row_b + at) = pack8<bf16_t, true>(u).a;
+                for (int k = 0; k < 8; ++k) t[k] = __uint_as_float(v[i * 8 + k]);
+                *reinterpret_cast<uint4*>(buf + lane * kRowB +
+                                          (swizzled_chunk<kRowB>(i, lane) << 4)) =
+                    pack8<bf16_t, true>(t).a;
             }
             if (!p.direct) {
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0 && inside && ok) {
-                    pt_store(&p.tm_out, smem_u32(buf), c0, r0);
-                    if (p.pre != nullptr) pt_store(&p.tm_pre, smem_u32(pres + (j & 1) * kBuf), c0, r0);
+                if (lane == 0) {
+                    if (in && ok) {
+                        pt_store(&p.tm_out, smem_u32(buf), c0, r0);
+                        if (p.pre != nullptr) pt_store(&p.tm_pre, smem_u32(pre), c0, r0);
+                    }
+                    bulk_commit_group();
                 }
-                if (lane == 0) bulk_commit_group();
             } else {
                 __syncwarp();
                 for (int r = 0; r < 32; ++r)
 #pragma unroll
                     for (int i = lane; i < kCh; i += 32) {
-                        const long long row = (long long)r0 + r, at = row * p.N + c0 + i;
-                        if (!inside || !ok || row >= p.M || c0 + i >= p.N) continue;
-                        const int off = r * kRowB + (swizzled_chunk<kRowB>(i >> 3, r) << 4) + (i & 7) * 2;
+                        const long long at_r = (long long)r0 + r, at = at_r * p.N + c0 + i;
+                        if (!in || !ok || at_r >= p.M || c0 + i >= p.N) continue;
+                        const int off =
+                            r * kRowB + (swizzled_chunk<kRowB>(i >> 3, r) << 4) + (i & 7) * 2;
                         if (!in_bounds(&g_block_status, p.out + at, 2, p.out, p.M * p.N * 2)) continue;
                         p.out[at] = *reinterpret_cast<const bf16_t*>(buf + off);
-                        if (p.pre != nullptr)
-                            p.pre[at] = *reinterpret_cast<const bf16_t*>(pres + (j & 1) * kBuf + off);
+                        if (p.pre != nullptr) p.pre[at] = *reinterpret_cast<const bf16_t*>(pre + off);
                     }
                 __syncwarp();
             }
+            turn ^= 1;
         }
     }
     if (lane == 0) bulk_wait_group0();  // stores complete before the block exits
@@ -284,24 +378,28 @@ pw_tc_kernel(const __grid_constant__ PtParams p) {
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int stages = p.stages, BN = p.BN, hB = BN / 2;
-    const int kB = pt_b_bytes(B_MN, BN), ch = pt_chunk(BN);
+    const int kB = pt_b_bytes(B_MN, BN);
     uint8_t* sA = smem;
     uint8_t* sB = smem + (size_t)stages * kPtA;
     uint8_t* staging = sB + (size_t)stages * kB;
-    float* bias_s = reinterpret_cast<float*>(
-        staging + (size_t)4 * 32 * ch * 2 * (p.n_bufs + (p.pre != nullptr ? 2 : 0)));
-    uint64_t* full_bar = reinterpret_cast<uint64_t*>(bias_s + BN);
+    PtShared sh;
+    sh.staging = staging;
+    sh.res = staging + (size_t)kPtEpiWarps * 32 * p.chunk * 2 * (p.n_bufs + p.n_pres);
+    sh.bias = reinterpret_cast<float*>(sh.res + (size_t)128 * p.chunk * 2 * p.res_bufs);
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(sh.bias + 2 * BN);
     uint64_t* empty_bar = full_bar + stages;
-    uint64_t* acc_full = empty_bar + stages;  // [2]
-    uint64_t* acc_empty = acc_full + 2;       // [2], used in the even CTA
-    uint64_t* res_bar = acc_empty + 2;        // [4 warps][4]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_bar + 16);
+    sh.acc_full = empty_bar + stages;  // [2]
+    sh.acc_empty = sh.acc_full + 2;    // [2], used in the even CTA
+    sh.bias_full = sh.acc_empty + 2;
+    sh.bias_empty = sh.bias_full + 2;
+    sh.res_full = sh.bias_empty + 2;   // [kPtResBufs]
+    sh.res_empty = sh.res_full + kPtResBufs;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sh.res_empty + kPtResBufs);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, G = gridDim.x >> 1;
-    const int total = p.tiles_m * p.tiles_n * p.splits;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
@@ -309,10 +407,15 @@ pw_tc_kernel(const __grid_constant__ PtParams p) {
             mbar_init(smem_u32(&empty_bar[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_u32(&acc_full[b]), 1);
-            mbar_init(smem_u32(&acc_empty[b]), 8);  // four epilogue warps of both CTAs
+            mbar_init(smem_u32(&sh.acc_full[b]), 1);
+            mbar_init(smem_u32(&sh.acc_empty[b]), 2 * kPtEpiWarps);  // of both CTAs
+            mbar_init(smem_u32(&sh.bias_full[b]), 1);
+            mbar_init(smem_u32(&sh.bias_empty[b]), kPtEpiWarps);
         }
-        for (int b = 0; b < 16; ++b) mbar_init(smem_u32(&res_bar[b]), 1);
+        for (int b = 0; b < kPtResBufs; ++b) {
+            mbar_init(smem_u32(&sh.res_full[b]), 1);
+            mbar_init(smem_u32(&sh.res_empty[b]), 4);  // the four warps whose turn the chunk is
+        }
         fence_mbar_init();
         tma_prefetch_desc(&p.tm_a);
         tma_prefetch_desc(&p.tm_b);
@@ -332,11 +435,11 @@ pw_tc_kernel(const __grid_constant__ PtParams p) {
             Ring ring;
             int issued = 0;
             bool ok = true;
-            for (int i = pair; i < total && ok; i += G) {
-                const PtItem t = pt_item(p, i);
+            for (PtWalk t(p, pair, G); t.left > 0 && ok; t.next(p)) {
                 const int m0 = t.m * kPtRows + (int)rank * 128;
                 const int n0 = t.n * BN + (int)rank * hB;
-                for (int kb = t.kb0; kb < t.kb1; ++kb, ++issued) {
+                const int kb1 = t.kb1(p);
+                for (int kb = t.kb0(p); kb < kb1; ++kb, ++issued) {
                     if (issued >= stages && !mbar_wait(smem_u32(&empty_bar[ring.st]), ring.ph ^ 1u,
                                                        &g_block_status, p.wait_limit_ns)) {
                         ok = false;
@@ -374,15 +477,15 @@ pw_tc_kernel(const __grid_constant__ PtParams p) {
             const uint64_t b0 = B_MN ? pt_desc_mn(smem_u32(sB)) : smem_desc_kmajor(smem_u32(sB), 128);
             Ring ring;
             bool ok = true;
-            for (int i = pair, it = 0; i < total && ok; i += G, ++it) {
-                const PtItem t = pt_item(p, i);
-                const int b = it & 1;
-                if (it >= 2 && !mbar_wait(smem_u32(&acc_empty[b]), (uint32_t)(((it >> 1) & 1) ^ 1),
-                                          &g_block_status, p.wait_limit_ns))
+            for (PtWalk t(p, pair, G); t.left > 0 && ok; t.next(p)) {
+                const int b = t.it & 1, kb0 = t.kb0(p), kb1 = t.kb1(p);
+                if (t.it >= 2 && !mbar_wait(smem_u32(&sh.acc_empty[b]),
+                                            (uint32_t)(((t.it >> 1) & 1) ^ 1), &g_block_status,
+                                            p.wait_limit_ns))
                     break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(b * BN);
-                for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(smem_u32(&full_bar[ring.st]), ring.ph, &g_block_status,
                                    p.wait_limit_ns)) {
                         ok = false;
@@ -394,21 +497,20 @@ pw_tc_kernel(const __grid_constant__ PtParams p) {
 #pragma unroll
                     for (int kk = 0; kk < kPtK / 16; ++kk)
                         umma_bf16_pair(d, a + a_step * kk, bd + b_step * kk, idesc,
-                                       kb == t.kb0 && kk == 0 ? 0u : 1u);
+                                       kb == kb0 && kk == 0 ? 0u : 1u);
                     umma_commit_pair(smem_u32(&empty_bar[ring.st]), (uint16_t)0x3);
                     ring.next(stages);
                 }
-                umma_commit_pair(smem_u32(&acc_full[b]), (uint16_t)0x3);
+                umma_commit_pair(smem_u32(&sh.acc_full[b]), (uint16_t)0x3);
             }
         }
         __syncwarp();
-    } else {
-        if (ch == 64)
-            pt_epilogue<64>(p, tmem_base, pair, G, total, rank, leader, warp, lane, staging, bias_s,
-                            acc_full, acc_empty, res_bar);
-        else
-            pt_epilogue<32>(p, tmem_base, pair, G, total, rank, leader, warp, lane, staging, bias_s,
-                            acc_full, acc_empty, res_bar);
+    } else if (warp == 2) {
+        if (p.chunk == 64) pt_ahead<64>(p, sh, pair, G, rank, lane);
+        else pt_ahead<32>(p, sh, pair, G, rank, lane);
+    } else if (warp >= 4) {
+        if (p.chunk == 64) pt_epilogue<64>(p, sh, tmem_base, pair, G, rank, leader, warp, lane);
+        else pt_epilogue<32>(p, sh, tmem_base, pair, G, rank, leader, warp, lane);
     }
     __syncwarp();
     tc_fence_before();
