@@ -208,7 +208,7 @@ SumShape sum_shape(long long M, int N) {
 // Shape of D(m, n) = sum over K on pw_tc_kernel.
 struct TcShape {
     int BN, tiles_m, tiles_n, kblocks, splits, kb_per_split, stages, chunk, n_bufs, n_pres, res_bufs,
-        tmem_cols, ldp;
+        n_acc, tmem_cols, ldp;
     size_t smem, ws;
 };
 
@@ -257,8 +257,9 @@ TcShape tc_shape(long long M, int N, long long K, bool b_mn, bool res, bool pre)
            pt_smem(b_mn, s.BN, s.stages, s.chunk, s.n_bufs + s.n_pres, s.res_bufs) > 227 * 1024)
         --s.stages;
     s.smem = pt_smem(b_mn, s.BN, s.stages, s.chunk, s.n_bufs + s.n_pres, s.res_bufs);
+    s.n_acc = std::min(kPtAccs, 512 / s.BN);
     s.tmem_cols = 32;
-    while (s.tmem_cols < 2 * s.BN) s.tmem_cols *= 2;
+    while (s.tmem_cols < s.n_acc * s.BN) s.tmem_cols *= 2;
     s.ws = parts ? pad256((size_t)s.splits * M * s.ldp * 4) : 0;
     return s;
 }
@@ -371,6 +372,7 @@ ccv3d_status run_tc(const void* A, int lda, const void* B, int ldb, long long M,
     p.kb_per_split = s.kb_per_split;
     p.stages = s.stages;
     p.chunk = s.chunk;
+    p.n_acc = s.n_acc;
     p.n_bufs = s.n_bufs;
     p.n_pres = s.n_pres;
     p.res_bufs = s.res_bufs;

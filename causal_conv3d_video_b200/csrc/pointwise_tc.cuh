@@ -39,6 +39,7 @@ constexpr int kPtEpiWarps = 8;
 // (a warp reads the TMEM lanes of its number modulo 4)
 constexpr int kPtThreads = 128 + 32 * kPtEpiWarps;
 constexpr int kPtResBufs = 4;    // chunks of the residual's ring
+constexpr int kPtAccs = 4;       // most accumulators (TMEM holds 512 columns)
 constexpr int kPtRows = 256;     // rows of a pair's tile
 constexpr int kPtK = 64;
 constexpr int kPtA = 128 * kPtK * 2;     // bytes of A a CTA and stage
@@ -56,6 +57,7 @@ struct PtParams {
     int chunk;               // columns the epilogue moves at a time: 64 or 32
     int n_bufs, n_pres;      // staging buffers of an epilogue warp
     int res_bufs;            // kPtResBufs, or 0 without a ring
+    int n_acc;               // accumulators in TMEM, 2 to kPtAccs
     int step_n, step_m, step_s;  // number of pairs, in tiles of the walk
     uint64_t wait_limit_ns;
 };
@@ -78,14 +80,27 @@ __device__ __forceinline__ void pt_store(const CUtensorMap* m, uint32_t src, int
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
                  ::"l"(reinterpret_cast<uint64_t>(m)), "r"(src), "r"(c0), "r"(c1) : "memory");
 }
+// True in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool pt_elect() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
 __device__ __forceinline__ uint32_t pt_mapa(uint32_t addr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// Arrive on another CTA's barrier.  No wider than CTA scope: what has to be
+// ordered before it are this warp's TMEM loads, which tcgen05.wait::ld and the
+// tcgen05 fence have completed; a cluster-scope release waited 3000 to 5000
+// cycles for the warp's outstanding stores.
 __device__ __forceinline__ void pt_arrive_remote(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
-                 : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // Shared-memory descriptor of an mn-major tile of 64 x 64 boxes (128-byte
@@ -104,7 +119,7 @@ __host__ __device__ constexpr size_t pt_smem(bool b_mn, int bn, int stages, int 
                                              int bufs, int res_bufs) {
     return 1024 + (size_t)stages * (kPtA + pt_b_bytes(b_mn, bn)) +
            (size_t)chunk * 2 * (kPtEpiWarps * 32 * bufs + 128 * res_bufs) +
-           (size_t)bn * 4 * 2 + (size_t)(2 * stages + 8 + 2 * kPtResBufs) * 8 + 16;
+           (size_t)bn * 4 * 2 + (size_t)(2 * stages + 2 * kPtAccs + 4 + 2 * kPtResBufs) * 8 + 16;
 }
 
 // A role's walk over its pair's work items: item i = (split, m, n), n fastest,
@@ -207,26 +222,27 @@ __device__ __forceinline__ void pt_epilogue(const PtParams& p, const PtShared& s
     const bool whole = p.partial == nullptr, biased = whole && p.bias != nullptr;
     int turn = 0;  // staging buffer
     int first = 0;  // chunks of the tiles before this one
+    Ring acc;
     bool ok = true;
-    for (PtWalk w(p, pair, G); w.left > 0; w.next(p), first += nch) {
-        const int b = w.it & 1;
-        const uint32_t round = (uint32_t)((w.it >> 1) & 1);
+    for (PtWalk w(p, pair, G); w.left > 0; w.next(p), first += nch, acc.next(p.n_acc)) {
+        const int b = w.it & 1;  // bias buffer
         const int r0 = w.m * kPtRows + (int)rank * 128 + q * 32;  // M < 2^31 - 256
         const int c_set = (set + first) & 1;
-        if (biased && ok && !mbar_wait(smem_u32(&sh.bias_full[b]), round, &g_block_status,
-                                       p.wait_limit_ns))
+        if (biased && ok && !mbar_wait(smem_u32(&sh.bias_full[b]), (uint32_t)((w.it >> 1) & 1),
+                                       &g_block_status, p.wait_limit_ns))
             ok = false;
-        if (ok && !mbar_wait(smem_u32(&sh.acc_full[b]), round, &g_block_status, p.wait_limit_ns))
+        if (ok && !mbar_wait(smem_u32(&sh.acc_full[acc.st]), acc.ph, &g_block_status,
+                             p.wait_limit_ns))
             ok = false;
         tc_fence_after();
-        const uint32_t tacc = tmem + (uint32_t)(b * p.BN) + ((uint32_t)(q * 32) << 16);
+        const uint32_t tacc = tmem + (uint32_t)(acc.st * p.BN) + ((uint32_t)(q * 32) << 16);
         const float* bias = sh.bias + b * p.BN;
         auto drained = [&]() {  // this warp has read the accumulator (and the bias)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (leader) mbar_arrive(smem_u32(&sh.acc_empty[b]));
-                else pt_arrive_remote(empty_leader + (uint32_t)(b * 8));
+                if (leader) mbar_arrive(smem_u32(&sh.acc_empty[acc.st]));
+                else pt_arrive_remote(empty_leader + (uint32_t)(acc.st * 8));
                 if (biased) mbar_arrive(smem_u32(&sh.bias_empty[b]));
             }
         };
@@ -388,9 +404,9 @@ pw_tc_kernel(const __grid_constant__ PtParams p) {
     sh.bias = reinterpret_cast<float*>(sh.res + (size_t)128 * p.chunk * 2 * p.res_bufs);
     uint64_t* full_bar = reinterpret_cast<uint64_t*>(sh.bias + 2 * BN);
     uint64_t* empty_bar = full_bar + stages;
-    sh.acc_full = empty_bar + stages;  // [2]
-    sh.acc_empty = sh.acc_full + 2;    // [2], used in the even CTA
-    sh.bias_full = sh.acc_empty + 2;
+    sh.acc_full = empty_bar + stages;      // [kPtAccs]
+    sh.acc_empty = sh.acc_full + kPtAccs;  // [kPtAccs], used in the even CTA
+    sh.bias_full = sh.acc_empty + kPtAccs;
     sh.bias_empty = sh.bias_full + 2;
     sh.res_full = sh.bias_empty + 2;   // [kPtResBufs]
     sh.res_empty = sh.res_full + kPtResBufs;
@@ -406,9 +422,11 @@ pw_tc_kernel(const __grid_constant__ PtParams p) {
             mbar_init(smem_u32(&full_bar[s]), 1);
             mbar_init(smem_u32(&empty_bar[s]), 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kPtAccs; ++b) {
             mbar_init(smem_u32(&sh.acc_full[b]), 1);
             mbar_init(smem_u32(&sh.acc_empty[b]), 2 * kPtEpiWarps);  // of both CTAs
+        }
+        for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&sh.bias_full[b]), 1);
             mbar_init(smem_u32(&sh.bias_empty[b]), kPtEpiWarps);
         }
@@ -467,7 +485,9 @@ pw_tc_kernel(const __grid_constant__ PtParams p) {
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
+            // The whole warp walks the loop and one elected lane issues: the
+            // descriptors stay in uniform registers, as the MMA takes them.
             const uint32_t idesc = idesc_bf16_m256((uint32_t)BN) | (A_MN ? 1u << 15 : 0u) |
                                    (B_MN ? 1u << 16 : 0u);
             // 16 of k further on: 32 bytes of a k-major row, two 1024-byte groups mn-major
@@ -475,33 +495,37 @@ pw_tc_kernel(const __grid_constant__ PtParams p) {
             constexpr uint32_t b_step = B_MN ? 2048 >> 4 : 32 >> 4;
             const uint64_t a0 = A_MN ? pt_desc_mn(smem_u32(sA)) : smem_desc_kmajor(smem_u32(sA), 128);
             const uint64_t b0 = B_MN ? pt_desc_mn(smem_u32(sB)) : smem_desc_kmajor(smem_u32(sB), 128);
-            Ring ring;
+            Ring ring, acc;
             bool ok = true;
-            for (PtWalk t(p, pair, G); t.left > 0 && ok; t.next(p)) {
-                const int b = t.it & 1, kb0 = t.kb0(p), kb1 = t.kb1(p);
-                if (t.it >= 2 && !mbar_wait(smem_u32(&sh.acc_empty[b]),
-                                            (uint32_t)(((t.it >> 1) & 1) ^ 1), &g_block_status,
-                                            p.wait_limit_ns))
-                    break;
+            for (PtWalk t(p, pair, G); t.left > 0 && ok; t.next(p), acc.next(p.n_acc)) {
+                const int kb0 = t.kb0(p), kb1 = t.kb1(p);
+                if (t.it >= p.n_acc) ok = mbar_wait(smem_u32(&sh.acc_empty[acc.st]), acc.ph ^ 1u,
+                                                    &g_block_status, p.wait_limit_ns);
+                if (!__all_sync(0xffffffffu, ok)) break;
                 tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(b * BN);
+                const uint32_t d = tmem_base + (uint32_t)(acc.st * BN);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(smem_u32(&full_bar[ring.st]), ring.ph, &g_block_status,
-                                   p.wait_limit_ns)) {
+                    ok = mbar_wait(smem_u32(&full_bar[ring.st]), ring.ph, &g_block_status,
+                                   p.wait_limit_ns);
+                    if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t a = a0 + (uint64_t)((ring.st * kPtA) >> 4);
                     const uint64_t bd = b0 + (uint64_t)((ring.st * kB) >> 4);
+                    if (pt_elect()) {
 #pragma unroll
-                    for (int kk = 0; kk < kPtK / 16; ++kk)
-                        umma_bf16_pair(d, a + a_step * kk, bd + b_step * kk, idesc,
-                                       kb == kb0 && kk == 0 ? 0u : 1u);
-                    umma_commit_pair(smem_u32(&empty_bar[ring.st]), (uint16_t)0x3);
+                        for (int kk = 0; kk < kPtK / 16; ++kk)
+                            umma_bf16_pair(d, a + a_step * kk, bd + b_step * kk, idesc,
+                                           kb == kb0 && kk == 0 ? 0u : 1u);
+                        umma_commit_pair(smem_u32(&empty_bar[ring.st]), (uint16_t)0x3);
+                        if (kb + 1 == kb1)
+                            umma_commit_pair(smem_u32(&sh.acc_full[acc.st]), (uint16_t)0x3);
+                    }
+                    __syncwarp();
                     ring.next(stages);
                 }
-                umma_commit_pair(smem_u32(&sh.acc_full[b]), (uint16_t)0x3);
             }
         }
         __syncwarp();
