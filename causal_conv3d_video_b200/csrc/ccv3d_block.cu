@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "ccv3d.h"
 #include "elem.cuh"
@@ -72,94 +73,171 @@ bool gate_fits(const ccv3d_norm_desc* d, const void* gate) {
     return gate == nullptr || (d->gate_rows >= 1 && d->rows % d->gate_rows == 0);
 }
 
-// Threads that share a row (0: the block's) and eight-channel units a thread:
-// the least idle shape of those the kernels are built for.  Single-channel
-// loads (C not a multiple of 8) want 16 threads side by side.
+// Threads that share a row (0: the block's) and eight-channel units a thread.
+// Within a warp the least idle of the shapes the kernels are built for (the
+// decoder's widths, three times a power of two, leave no thread idle), of
+// equals the one with the most threads a row; single-channel loads (C not a
+// multiple of 8) want 16 threads side by side.  Wider rows take a block each.
 struct RowShape {
     int tpr, units, threads;
 };
 RowShape row_shape(int C, bool vec, int max_units) {
     const int n = (int)up(C, 8);
-    for (int tpr = vec ? 4 : 16; tpr <= 32; tpr *= 2)
-        for (int u = 1; u <= max_units; ++u)
-            if (tpr * u >= n) return {tpr, u, 128};
-    const int u = n > 512 ? 2 : 1;
-    return {0, u, (int)up(up(n, u), 32) * 32};
+    RowShape best = {0, n > 512 ? 2 : 1, 0};
+    best.threads = (int)up(up(n, best.units), 32) * 32;
+    int cover = 1 << 30;
+    for (int u = 1; u <= max_units; ++u)
+        for (int tpr = vec ? 4 : 16; tpr <= 32; tpr *= 2)
+            if (tpr * u >= n && tpr * u < cover) {
+                cover = tpr * u;
+                best = {tpr, u, 0};
+            }
+    return best;
 }
 
-template <typename T, bool V, int TPR>
-void norm_fwd_units(const NormFwd& p, const RowShape& s, int grid, cudaStream_t st) {
-    switch (s.units) {
-        case 1: norm_fwd_kernel<T, V, TPR, 1><<<grid, s.threads, 0, st>>>(p); break;
-        case 2: norm_fwd_kernel<T, V, TPR, 2><<<grid, s.threads, 0, st>>>(p); break;
-        default:
-            if constexpr (TPR != 0) norm_fwd_kernel<T, V, TPR, 3><<<grid, s.threads, 0, st>>>(p);
+// Tiles of rows for the staged kernels: about `want` bytes of all tensors a
+// stage, whole passes of the block, and no more rows than there are.  Long rows
+// (fp32 at the decoder's wide layers) take blocks of fewer threads, so that a
+// pass stays near that size too.
+struct TileLaunch {
+    TileShape t;
+    int threads, blocks_per_sm;
+    size_t smem;
+};
+TileLaunch tile_launch(const RowShape& r, int C, int e, long long rows, int tensors, int vectors,
+                       int want, int threads_per_sm) {
+    TileLaunch l;
+    const int row = C * e;
+    l.threads = kTileThreads;
+    while (l.threads > 64 && (long long)tensors * row * (l.threads / r.tpr) > want) l.threads /= 2;
+    const int pass = l.threads / r.tpr;
+    long long passes =
+        std::max<long long>(1, (long long)want * l.threads / kTileThreads / ((long long)tensors * row * pass));
+    // (short calls: about four tiles a block, so that the blocks end together)
+    passes = std::max<long long>(1, std::min(passes, rows / ((long long)pass * kSms * 8)));
+    l.t.rows = (int)passes * pass;
+    l.t.cap = (l.t.rows * row + 16 + 127) / 128 * 128;
+    l.t.vec_len = r.tpr * r.units * 8;
+    l.t.stages = (long long)tensors * l.t.cap * 3 <= 100 * 1024 ? 3 : 2;
+    l.smem = (size_t)l.t.stages * tensors * l.t.cap + (size_t)vectors * l.t.vec_len * 4 + l.t.stages * 8;
+    // (the column sums' buffer of the backward pass, a row a warp, is the idle ring)
+    l.smem = std::max(l.smem, (size_t)(l.threads / 32) * C * 4);
+    l.blocks_per_sm = (int)std::max<size_t>(
+        1, std::min<size_t>(threads_per_sm / l.threads, 227 * 1024 / (l.smem + 1024)));
+    return l;
+}
+
+// Dynamic shared memory of up to 200 KB for a kernel, once per device.
+template <auto* K>
+void allow_smem() {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> done[kDevices];
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) {
+        cudaGetLastError();
+        return;
+    }
+    if (done[dev].load(std::memory_order_acquire)) return;
+    cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    cudaGetLastError();
+    done[dev].store(true, std::memory_order_release);
+}
+
+template <typename T, bool V, bool B, int TPR, int NU>
+void norm_fwd_run(const NormFwd& p, const RowShape& r, cudaStream_t st) {
+    if constexpr (TPR == 0) {
+        const int grid = (int)std::min<long long>(p.rows, (long long)kSms * std::max(1, 1024 / r.threads));
+        norm_fwd_rows<T, V, NU, B><<<grid, r.threads, 0, st>>>(p);
+    } else {
+        const TileLaunch l = tile_launch(r, p.C, sizeof(T), p.rows, B ? 2 : 1, 4, 20 * 1024, 768);
+        const int grid = (int)std::min<long long>(up(p.rows, l.t.rows), kSms * l.blocks_per_sm);
+        allow_smem<norm_fwd_tiles<T, V, TPR, NU, B>>();
+        norm_fwd_tiles<T, V, TPR, NU, B><<<grid, l.threads, l.smem, st>>>(p, l.t);
     }
 }
 
-template <typename T, bool V>
-void norm_fwd_shape(const NormFwd& p, cudaStream_t st) {
-    const RowShape s = row_shape(p.C, V, 3);
-    const long long rpb = s.tpr == 0 ? 1 : s.threads / s.tpr;
-    const int grid = (int)std::min<long long>(up(p.rows, rpb), (long long)kSms * 64);
-    switch (s.tpr) {
-        case 4: if constexpr (V) norm_fwd_units<T, V, 4>(p, s, grid, st); break;
-        case 8: if constexpr (V) norm_fwd_units<T, V, 8>(p, s, grid, st); break;
-        case 16: norm_fwd_units<T, V, 16>(p, s, grid, st); break;
-        case 32: norm_fwd_units<T, V, 32>(p, s, grid, st); break;
-        default: norm_fwd_units<T, V, 0>(p, s, grid, st);
-    }
-}
+// Units a thread at most, backward: the general form's four column sums leave
+// registers for two.
+constexpr int bwd_units(bool gen) { return gen ? 2 : 3; }
 
 // Launch shape of the backward pass: blocks per gate group.
 struct BwdShape {
     RowShape row;
+    TileLaunch tile;
     long long groups, group_rows;
     int blocks_per_group;
 };
-BwdShape bwd_shape(const ccv3d_norm_desc* d, bool gated) {
-    BwdShape b;
-    b.row = row_shape(d->C, d->C % 8 == 0, 2);
+BwdShape bwd_shape(const ccv3d_norm_desc* d, bool gated, bool gen) {
+    BwdShape b = {};
+    b.row = row_shape(d->C, d->C % 8 == 0, bwd_units(gen));
     b.groups = gated ? d->rows / d->gate_rows : 1;
     b.group_rows = gated ? d->gate_rows : d->rows;
-    // short groups: fewer rows side by side, so that no thread is left without one
-    if (b.row.tpr != 0)
-        while (b.row.threads > 32 && b.row.threads / 2 / b.row.tpr >= b.group_rows)
-            b.row.threads /= 2;
-    const long long rpb = b.row.tpr == 0 ? 1 : b.row.threads / b.row.tpr;
-    const long long most = std::max<long long>(1, (long long)kSms * 8 / b.groups);
-    b.blocks_per_group = (int)std::max<long long>(1, std::min(most, up(b.group_rows, rpb * 4)));
+    long long steps = b.group_rows, blocks;
+    if (b.row.tpr == 0) {
+        blocks = (long long)kSms * std::max(1, 512 / b.row.threads);
+    } else {
+        b.tile = tile_launch(b.row, d->C, (int)size_of(d->dtype), b.group_rows, 4, 3, 52 * 1024, 512);
+        blocks = kSms * b.tile.blocks_per_sm;
+        steps = up(b.group_rows, b.tile.t.rows);
+    }
+    b.blocks_per_group = (int)std::min(steps, std::max<long long>(1, blocks / b.groups));
     return b;
 }
 
-template <typename T, bool V, int TPR, bool B>
-void norm_bwd_units(const NormBwd& p, const BwdShape& s, int grid, cudaStream_t st) {
-    const size_t smem = TPR == 0 ? 0 : (size_t)(s.row.threads / 32) * p.C * 4;
-    if (s.row.units == 1)
-        norm_bwd_kernel<T, V, TPR, 1, B><<<grid, s.row.threads, smem, st>>>(p);
-    else
-        norm_bwd_kernel<T, V, TPR, 2, B><<<grid, s.row.threads, smem, st>>>(p);
-}
-
-template <typename T, bool V, bool B>
-void norm_bwd_shape(const NormBwd& p, const BwdShape& s, int grid, cudaStream_t st) {
-    switch (s.row.tpr) {
-        case 4: if constexpr (V) norm_bwd_units<T, V, 4, B>(p, s, grid, st); break;
-        case 8: if constexpr (V) norm_bwd_units<T, V, 8, B>(p, s, grid, st); break;
-        case 16: norm_bwd_units<T, V, 16, B>(p, s, grid, st); break;
-        case 32: norm_bwd_units<T, V, 32, B>(p, s, grid, st); break;
-        default: norm_bwd_units<T, V, 0, B>(p, s, grid, st);
+template <typename T, bool V, bool B, int TPR, int NU>
+void norm_bwd_run(const NormBwd& p, const BwdShape& s, cudaStream_t st) {
+    const int grid = (int)(s.groups * s.blocks_per_group);
+    if constexpr (TPR == 0) {
+        norm_bwd_rows<T, V, NU, B><<<grid, s.row.threads, 0, st>>>(p);
+    } else {
+        allow_smem<norm_bwd_tiles<T, V, TPR, NU, B>>();
+        norm_bwd_tiles<T, V, TPR, NU, B><<<grid, s.tile.threads, s.tile.smem, st>>>(p, s.tile.t);
     }
 }
 
+// Calls f with the constants (TPR, units) of a shape.
+template <bool V, int U, typename F>
+void with_shape(const RowShape& r, F&& f) {
+    auto units = [&](auto tpr) {
+        if (r.units == 1) f(tpr, std::integral_constant<int, 1>());
+        else if (r.units == 2) f(tpr, std::integral_constant<int, 2>());
+        else if constexpr (U > 2 && decltype(tpr)::value != 0) f(tpr, std::integral_constant<int, 3>());
+    };
+    switch (r.tpr) {
+        case 4: if constexpr (V) units(std::integral_constant<int, 4>()); break;
+        case 8: if constexpr (V) units(std::integral_constant<int, 8>()); break;
+        case 16: units(std::integral_constant<int, 16>()); break;
+        case 32: units(std::integral_constant<int, 32>()); break;
+        default: units(std::integral_constant<int, 0>());
+    }
+}
+
+template <typename T, bool V, bool B>
+void norm_fwd_shape(const NormFwd& p, cudaStream_t st) {
+    // few rows (under two an SM): a block each, without the ring's start-up
+    // (one row of 768: 3.3 us against 5.7)
+    const RowShape r = row_shape(p.C, V, p.rows < 2 * kSms ? 0 : 3);
+    with_shape<V, 3>(r, [&](auto tpr, auto nu) { norm_fwd_run<T, V, B, tpr(), nu()>(p, r, st); });
+}
+template <typename T, bool V, bool B>
+void norm_bwd_shape(const NormBwd& p, const BwdShape& s, cudaStream_t st) {
+    with_shape<V, bwd_units(B)>(s.row, [&](auto tpr, auto nu) { norm_bwd_run<T, V, B, tpr(), nu()>(p, s, st); });
+}
+
 template <typename T>
-void norm_bwd_type(const NormBwd& p, const BwdShape& s, bool bias, int grid, cudaStream_t st) {
+void norm_fwd_type(const NormFwd& p, cudaStream_t st) {
     if (p.C % 8 == 0)
-        bias ? norm_bwd_shape<T, true, true>(p, s, grid, st)
-             : norm_bwd_shape<T, true, false>(p, s, grid, st);
+        p.b != nullptr ? norm_fwd_shape<T, true, true>(p, st) : norm_fwd_shape<T, true, false>(p, st);
     else
-        bias ? norm_bwd_shape<T, false, true>(p, s, grid, st)
-             : norm_bwd_shape<T, false, false>(p, s, grid, st);
+        p.b != nullptr ? norm_fwd_shape<T, false, true>(p, st)
+                       : norm_fwd_shape<T, false, false>(p, st);
+}
+template <typename T>
+void norm_bwd_type(const NormBwd& p, const BwdShape& s, bool gen, cudaStream_t st) {
+    if (p.C % 8 == 0)
+        gen ? norm_bwd_shape<T, true, true>(p, s, st) : norm_bwd_shape<T, true, false>(p, s, st);
+    else
+        gen ? norm_bwd_shape<T, false, true>(p, s, st) : norm_bwd_shape<T, false, false>(p, s, st);
 }
 
 // --------------------------------------------------------------- pointwise
@@ -175,14 +253,34 @@ ccv3d_status check_pointwise(const ccv3d_pointwise_desc* d) {
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Splits of the reduction on FFMA: enough blocks for the SMs, each with at
-// least 8 steps of 16.
-int simt_splits(long long M, long long N, long long K) {
-    const long long tiles = up(M, kPwTile) * up(N, kPwTile);
-    return (int)std::max<long long>(1, std::min<long long>({2 * kSms / tiles, up(K, 128), 512}));
+// Shape of a product on FFMA: tiles of 128, or of 64 where less of them is lost
+// at the edges or in the last wave (a 64-wide tile's time counts 1.4 times its
+// share of a 128-wide one's: half the FMAs per shared-memory read), and splits of
+// the reduction while that leaves SMs without a block, of at least 8 steps of 16.
+struct SimtShape {
+    int tile, splits;
+    long long tiles, k_per_split;
+};
+SimtShape simt_shape(long long M, long long N, long long K) {
+    SimtShape best = {};
+    double cost = 1e300;
+    for (int t : {128, 64}) {
+        const long long tiles = up(M, t) * up(N, t);
+        const int want = (int)std::max<long long>(1, std::min<long long>({2 * kSms / tiles, up(K, 128), 512}));
+        const long long per = up(up(K, want), kPwK) * kPwK;
+        const int splits = (int)std::max<long long>(1, up(K, per));
+        const int resident = t == 128 ? 1 : 4;  // blocks an SM, in equal shares of its time
+        const double c = std::ceil((double)tiles * splits / (kSms * resident)) * resident *
+                         (double)t * t * (per + 32) * (t == 128 ? 1.0 : 1.4);
+        if (c < cost) {
+            cost = c;
+            best = {t, splits, tiles, per};
+        }
+    }
+    return best;
 }
 size_t simt_ws(long long M, long long N, long long K) {
-    const int s = simt_splits(M, N, K);
+    const int s = simt_shape(M, N, K).splits;
     return s > 1 ? pad256((size_t)s * M * N * 4) : 0;
 }
 
@@ -454,14 +552,15 @@ ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb
     p.N = N;
     p.K = K;
     p.vec = lda % 4 == 0 && ldb % 4 == 0;
-    p.splits = simt_splits(M, N, K);
-    p.k_per_split = up(up(K, p.splits), kPwK) * kPwK;
-    p.splits = (int)std::max<long long>(1, up(K, p.k_per_split));
+    const SimtShape s = simt_shape(M, N, K);
+    p.splits = s.splits;
+    p.k_per_split = s.k_per_split;
     p.o = o;
     p.o.partial = p.splits > 1 ? partial : nullptr;
-    const long long tiles = up(M, kPwTile) * up(N, kPwTile);
-    if (tiles > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;
-    pw_simt_kernel<float, AK, BK><<<dim3((unsigned)tiles, 1, p.splits), 256, 0, st>>>(p);
+    if (s.tiles > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)s.tiles, 1, p.splits);
+    if (s.tile == 128) pw_simt_kernel<float, AK, BK, 128><<<grid, 256, 0, st>>>(p);
+    else pw_simt_kernel<float, AK, BK, 64><<<grid, 256, 0, st>>>(p);
     if (p.splits > 1) {
         const long long blocks = std::min<long long>(up(M * N, 256), kSms * 16LL);
         pw_join_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(partial, p.splits, N, o);
@@ -586,10 +685,23 @@ QCacheJob qcache_job(const ccv3d_qcache_desc* d) {
 
 // Whole frames on the grid's second axis (at most 65535 of them).
 dim3 qcache_grid(const QCacheJob& j, long long threads_a_pixel) {
-    const long long frames = (long long)j.N * j.frames;
-    const long long want = std::max<long long>(1, kSms * 32LL / frames);
-    return dim3((unsigned)std::min<long long>(up(j.pixels * threads_a_pixel, 256), want),
-                (unsigned)frames);
+    return dim3((unsigned)up(j.pixels * threads_a_pixel, kQThreads * kQUnits),
+                (unsigned)(j.N * j.frames));
+}
+
+template <typename T>
+void qcache_write_run(const QCacheJob& j, int fmt, cudaStream_t st) {
+    const dim3 grid = qcache_grid(j, 4LL * j.groups);
+    if (j.C % 32 == 0) qcache_write_kernel<T, true, true><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else if (j.C % 8 == 0) qcache_write_kernel<T, true, false><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else qcache_write_kernel<T, false, false><<<grid, kQThreads, 0, st>>>(j, fmt);
+}
+template <typename T>
+void qcache_read_run(const QCacheJob& j, int fmt, cudaStream_t st) {
+    const dim3 grid = qcache_grid(j, up(j.C, 8));
+    if (j.C % 32 == 0) qcache_read_kernel<T, true, true><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else if (j.C % 8 == 0) qcache_read_kernel<T, true, false><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else qcache_read_kernel<T, false, false><<<grid, kQThreads, 0, st>>>(j, fmt);
 }
 
 }  // namespace
@@ -622,26 +734,23 @@ ccv3d_status ccv3d_norm_forward(const ccv3d_norm_desc* d, const void* h, const v
     const ccv3d_status k = bufs.check();
     if (k != CCV3D_OK) return k;
     const NormFwd p = {h, b, gate, post_w, post_bias, pre_w, pre_bias, h_out, y,
-                       d->rows, gate != nullptr ? d->gate_rows : 1, d->C, d->pre, d->post, d->act,
+                       d->rows, gate != nullptr ? d->gate_rows : d->rows, d->C, d->pre, d->post, d->act,
                        d->eps, d->scale, 1.0f / (float)d->C};
-    const bool v = d->C % 8 == 0;
-    if (d->dtype == CCV3D_BF16)
-        v ? norm_fwd_shape<bf16, true>(p, stream) : norm_fwd_shape<bf16, false>(p, stream);
-    else
-        v ? norm_fwd_shape<float, true>(p, stream) : norm_fwd_shape<float, false>(p, stream);
+    d->dtype == CCV3D_BF16 ? norm_fwd_type<bf16>(p, stream) : norm_fwd_type<float>(p, stream);
     return launched();
 }
 
 size_t ccv3d_norm_workspace(const ccv3d_norm_desc* d) {
     if (check_norm(d) != CCV3D_OK || d->rows == 0) return 0;
-    // a call with a gate and one without may both follow: the larger of the two
+    // with a gate or without one, with biases or without: the largest of them
     long long slots = 0;
-    for (int gated = 0; gated < 2; ++gated) {
+    for (int form = 0; form < 4; ++form) {
+        const bool gated = form & 1, gen = form & 2;
         if (gated && (d->gate_rows < 1 || d->rows % d->gate_rows != 0)) continue;
-        const BwdShape b = bwd_shape(d, gated != 0);
-        slots = std::max(slots, b.groups * b.blocks_per_group);
+        const BwdShape b = bwd_shape(d, gated, gen);
+        slots = std::max(slots, b.groups * b.blocks_per_group * (gen ? 4 : 2));
     }
-    return (size_t)slots * d->C * 4 * sizeof(float);
+    return (size_t)slots * d->C * sizeof(float);
 }
 
 ccv3d_status ccv3d_norm_backward(const ccv3d_norm_desc* d, const void* h_out, const void* b,
@@ -689,26 +798,27 @@ ccv3d_status ccv3d_norm_backward(const ccv3d_norm_desc* d, const void* h_out, co
     bufs.out(ws, need);
     const ccv3d_status k = bufs.check();
     if (k != CCV3D_OK) return k;
-    const BwdShape s = bwd_shape(d, gate != nullptr);
+    // the general form: biases, whose gradients (and dgate, to which post_bias adds) are
+    // sums of du and G, or layer norms
+    const bool bias = pre_bias != nullptr || post_bias != nullptr ||
+                      d->pre == CCV3D_NORM_LAYER || d->post == CCV3D_NORM_LAYER;
+    const BwdShape s = bwd_shape(d, gate != nullptr, bias);
     const long long slots = s.groups * s.blocks_per_group;
     if (slots > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;
-    // sums of du and G are wanted for bias gradients, and for dgate where a bias adds to it
-    const bool bias = dpre_bias != nullptr || dpost_bias != nullptr ||
-                      (dgate != nullptr && post_bias != nullptr);
     const NormBwd p = {h_out, b, gate, post_w, post_bias, pre_w, pre_bias, dy, dh_out, dh, db,
                        sums ? static_cast<float*>(ws) : nullptr, d->rows, s.group_rows, s.groups,
                        slots, s.blocks_per_group, d->C, d->pre, d->post, d->act, d->eps, d->scale,
                        1.0f / (float)d->C};
-    if (d->dtype == CCV3D_BF16) norm_bwd_type<bf16>(p, s, bias, (int)slots, stream);
-    else norm_bwd_type<float>(p, s, bias, (int)slots, stream);
+    if (d->dtype == CCV3D_BF16) norm_bwd_type<bf16>(p, s, bias, stream);
+    else norm_bwd_type<float>(p, s, bias, stream);
     if (launched() != CCV3D_OK) return CCV3D_ERR_CUDA;
     if (!sums) return CCV3D_OK;
     float* part = static_cast<float*>(ws);
     const NormFin f = {part, part, gate, post_w, post_bias, dgate, dpost_w, dpost_bias, dpre_w,
                        dpre_bias, s.groups, slots, s.blocks_per_group, d->C, bias ? 1 : 0,
                        b != nullptr ? 1 : 0, d->scale};
-    const dim3 grid((unsigned)up(d->C, 32), (unsigned)std::min<long long>(s.groups, 32768));
-    const dim3 block(32, 32);
+    const dim3 grid((unsigned)up(d->C, kFinCols), (unsigned)std::min<long long>(s.groups, 32768));
+    const dim3 block(kFinCols, kFinRows);
     if (d->dtype == CCV3D_BF16) {
         norm_fin_group_kernel<bf16><<<grid, block, 0, stream>>>(f);
         if (s.groups > 1) norm_fin_all_kernel<bf16><<<grid.x, block, 0, stream>>>(f);
@@ -835,15 +945,8 @@ ccv3d_status ccv3d_qcache_write(const ccv3d_qcache_desc* d, const void* x, int T
     j.first = first;
     j.frames = frames;
     j.slot = slot;
-    const dim3 grid = qcache_grid(j, 4LL * j.groups);
-    const bool v = d->C % 8 == 0;
-    if (d->dtype == CCV3D_BF16) {
-        if (v) qcache_write_kernel<bf16, true><<<grid, 256, 0, stream>>>(j, d->format);
-        else qcache_write_kernel<bf16, false><<<grid, 256, 0, stream>>>(j, d->format);
-    } else {
-        if (v) qcache_write_kernel<float, true><<<grid, 256, 0, stream>>>(j, d->format);
-        else qcache_write_kernel<float, false><<<grid, 256, 0, stream>>>(j, d->format);
-    }
+    d->dtype == CCV3D_BF16 ? qcache_write_run<bf16>(j, d->format, stream)
+                           : qcache_write_run<float>(j, d->format, stream);
     return launched();
 }
 
@@ -869,15 +972,8 @@ ccv3d_status ccv3d_qcache_read(const ccv3d_qcache_desc* d, const void* codes, co
     j.scales = static_cast<uint8_t*>(const_cast<void*>(scales));
     j.frames = frames;
     j.slot = head;
-    const dim3 grid = qcache_grid(j, up(d->C, 8));
-    const bool v = d->C % 8 == 0;
-    if (d->dtype == CCV3D_BF16) {
-        if (v) qcache_read_kernel<bf16, true><<<grid, 256, 0, stream>>>(j, d->format);
-        else qcache_read_kernel<bf16, false><<<grid, 256, 0, stream>>>(j, d->format);
-    } else {
-        if (v) qcache_read_kernel<float, true><<<grid, 256, 0, stream>>>(j, d->format);
-        else qcache_read_kernel<float, false><<<grid, 256, 0, stream>>>(j, d->format);
-    }
+    d->dtype == CCV3D_BF16 ? qcache_read_run<bf16>(j, d->format, stream)
+                           : qcache_read_run<float>(j, d->format, stream);
     return launched();
 }
 

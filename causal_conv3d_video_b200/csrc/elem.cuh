@@ -33,23 +33,20 @@ constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
 // act(u); GELU in its tanh form, 0.5 u (1 + tanh z) = u * sigmoid(2 z).
-// (-inf and values whose sigmoid underflows give -0 or 0, not NaN: the
-// product is taken only where the sigmoid is not zero.)
 template <typename T>
 __device__ __forceinline__ float act_of(float u, int kind) {
     if (kind == kActNone) return u;
-    const float s = sigmoid_of<T>(kind == kActSilu ? u : 2.0f * kGeluC * (u + kGeluA * u * u * u));
-    return s == 0.0f ? 0.0f : u * s;
+    return u * sigmoid_of<T>(kind == kActSilu ? u : 2.0f * kGeluC * (u + kGeluA * u * u * u));
 }
 
-// act'(u): SiLU s (1 + u (1 - s)); GELU s + u s (1 - s) 2 z'(u).
+// act'(u): SiLU s (1 + u (1 - s)); GELU s + u s (1 - s) 2 z'(u), whose last
+// factor may overflow where s (1 - s) is 0.
 template <typename T>
 __device__ __forceinline__ float act_grad_of(float u, int kind) {
     if (kind == kActNone) return 1.0f;
     if (kind == kActSilu) {
         const float s = sigmoid_of<T>(u);
-        const float t = 1.0f - s;
-        return s == 0.0f ? 0.0f : (t == 0.0f ? s : s * (1.0f + u * t));
+        return s * fmaf(u, 1.0f - s, 1.0f);
     }
     const float s = sigmoid_of<T>(2.0f * kGeluC * (u + kGeluA * u * u * u));
     const float t = s * (1.0f - s);
@@ -158,6 +155,97 @@ __device__ __forceinline__ void store8(const Raw8<T, V>& r, T* row, int c0, int 
             *reinterpret_cast<float4*>(row + c0 + 4) = r.b;
         }
     }
+}
+
+// ------------------------------------------------------- pairs of fp32 values
+// Two fp32 values in a 64-bit register: one instruction multiplies, adds or
+// fuses both (each rounded as the single one would be), which halves the
+// arithmetic of the row kernels.
+typedef unsigned long long f2;
+
+__device__ __forceinline__ f2 f2_make(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_all(float a) { return f2_make(a, a); }
+__device__ __forceinline__ void f2_get(f2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+    float a, b;
+    f2_get(v, a, b);
+    return a + b;
+}
+
+// Eight channels as four pairs.
+template <typename T, bool V>
+__device__ __forceinline__ void unpack8(const Raw8<T, V>& r, f2 (&f)[4]) {
+    float t[8];
+    unpack8<T, V>(r, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2_make(t[2 * i], t[2 * i + 1]);
+}
+template <typename T, bool V>
+__device__ __forceinline__ Raw8<T, V> pack8(const f2 (&f)[4]) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_get(f[i], t[2 * i], t[2 * i + 1]);
+    return pack8<T, V>(t);
+}
+
+// sigmoid of both, as sigmoid_of.
+template <typename T>
+__device__ __forceinline__ f2 f2_sigmoid(f2 v) {
+    float a, b;
+    if constexpr (sizeof(T) == 2) {
+        f2_get(f2_mul(v, f2_all(-1.4426950408889634f)), a, b);  // exp(-v) = 2^(-v log2 e)
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+        f2_get(f2_add(f2_make(a, b), f2_all(1.0f)), a, b);
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+        return f2_make(a, b);
+    } else {
+        f2_get(v, a, b);
+        return f2_make(sigmoid_of<T>(a), sigmoid_of<T>(b));
+    }
+}
+// v act-transformed, as act_of.
+template <typename T>
+__device__ __forceinline__ f2 f2_act(f2 u, int kind) {
+    if (kind == kActNone) return u;
+    if (kind == kActSilu) return f2_mul(u, f2_sigmoid<T>(u));
+    const f2 u3 = f2_mul(f2_mul(u, u), u);
+    return f2_mul(u, f2_sigmoid<T>(f2_mul(f2_all(2.0f * kGeluC), f2_fma(u3, f2_all(kGeluA), u))));
+}
+// act', as act_grad_of.
+template <typename T>
+__device__ __forceinline__ f2 f2_act_grad(f2 u, int kind) {
+    const f2 one = f2_all(1.0f);
+    if (kind == kActNone) return one;
+    if (kind == kActSilu) {
+        const f2 s = f2_sigmoid<T>(u);
+        return f2_mul(s, f2_fma(u, f2_fma(s, f2_all(-1.0f), one), one));
+    }
+    float a, b;
+    f2_get(u, a, b);
+    return f2_make(act_grad_of<T>(a, kActGelu), act_grad_of<T>(b, kActGelu));
 }
 
 }  // namespace ccv3d

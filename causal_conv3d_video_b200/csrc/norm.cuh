@@ -20,14 +20,24 @@
 // rows, then go through fp32 partials that a second launch adds in a fixed
 // order: no atomics, the same bits every run.
 //
-// HBM-bound (2 to 4 tensors moved forward, 4 to 6 backward, about 20 flops
-// an element): a row is read once and stays in registers.  TPR threads share
-// a row (a power of two within a warp, or the whole block for wide rows), so
-// that the row statistics are a few shuffles and each thread keeps a fixed
-// set of channels, whose weights it reads once per block and whose column
-// sums it owns.
+// HBM-bound (2 to 4 tensors moved forward, 4 to 6 backward): a row is read
+// once and stays in registers.  TPR threads share a row (a power of two within
+// a warp, or the whole block for wide rows), so that the row statistics are a
+// few shuffles and each thread keeps a fixed set of channels, whose column sums
+// it owns.
+//   * Rows within a warp's share (the decoder's widths): blocks walk tiles of
+//     rows; one thread has the next tiles copied to shared memory (bulk copies
+//     on an mbarrier ring, rows are contiguous) while all work on this one, so
+//     that the bytes in flight do not hang on registers or occupancy, and an
+//     odd channel count costs no unaligned global loads.  The vectors (gate,
+//     weights, biases, with the residual scale multiplied in) are in shared
+//     memory as fp32.
+//   * Wider rows: a block a row, loads straight to registers, the next row's
+//     in flight while this one is worked on.
 #pragma once
 #include "elem.cuh"
+#include "params.h"
+#include "ptx.cuh"
 
 namespace ccv3d {
 
@@ -120,79 +130,100 @@ __device__ __forceinline__ float normalise(float (&v)[NU][8], int kind, int lane
     return rstd;
 }
 
-// v = v * w + bias over a unit; a NULL w is ones, a NULL bias zeros.
+// Channels c0 .. of a weight vector as fp32; `otherwise` where there is none,
+// 0 past C (so that idle lanes add nothing to a row's sums).
 template <typename T, bool V>
-__device__ __forceinline__ void affine8(float (&v)[8], const T* w, const T* bias, int c0,
-                                        int step, int C) {
+__device__ __forceinline__ void weights8(float (&f)[8], const T* w, float otherwise, int c0,
+                                         int step, int C) {
     if (w != nullptr) {
         Raw8<T, V> r;
-        float f[8];
         load8<T, V>(r, w, c0, step, C);
         unpack8<T, V>(r, f);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= f[i];
-    }
-    if (bias != nullptr) {
-        Raw8<T, V> r;
-        float f[8];
-        load8<T, V>(r, bias, c0, step, C);
-        unpack8<T, V>(r, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += f[i];
+        for (int i = 0; i < 8; ++i) f[i] = (V ? c0 : c0 + i * step) < C ? otherwise : 0.0f;
     }
 }
 
-// Rows wider than a warp's share: at most 512 threads a row, so that a thread
-// may hold 128 registers.
-constexpr int norm_threads(int tpr) { return tpr == 0 ? 512 : 128; }
-
-template <typename T, bool V, int TPR, int NU>
-__global__ void __launch_bounds__(norm_threads(TPR)) norm_fwd_kernel(const __grid_constant__ NormFwd p) {
+// The wide-row form, one block a row (TPR = 0).  kB: there is a block output b
+// (its norm, gate and scale); otherwise only the norm and activation of h.
+template <typename T, bool V, int NU, bool kB>
+__global__ void __launch_bounds__(512) norm_fwd_rows(
+    const __grid_constant__ NormFwd p) {
     __shared__ float red[2][4][32];
     int turn = 0;
-    const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
-    const int lane = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % tpr;
-    const int rpb = (int)blockDim.x / tpr;
+    constexpr int TPR = 0;
+    const int tpr = (int)blockDim.x, lane = (int)threadIdx.x;
     const int C = p.C;
-    const long long tensor = p.rows * C * (long long)sizeof(T);
-    for (long long base = (long long)blockIdx.x * rpb; base < p.rows;
-         base += (long long)gridDim.x * rpb) {
-        const long long row = base + (int)threadIdx.x / tpr;
-        const bool valid = row < p.rows;  // threads of a tail row still take part in the shuffles
-        const long long at = (valid ? row : 0) * C;
-        const T* h = static_cast<const T*>(p.h) + at;
-        const bool ok = valid && in_bounds(&g_block_status, h, (long long)C * sizeof(T), p.h, tensor);
-        Raw8<T, V> rh[NU], rb[NU];
+    const long long tensor = p.rows * C * (long long)sizeof(T), stride = gridDim.x;
+    const T *h = static_cast<const T*>(p.h), *b = static_cast<const T*>(p.b);
+    // what each thread keeps of the vectors
+    float w[NU][8], wb[NU][8], g[NU][8], gb[NU][8];
+    long long gate_row = -1;
+    auto gates = [&](long long row) {  // scale * gate * post_w, scale * gate * post_bias
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
             const int c0 = unit_c0<V>(u, lane, tpr);
-            if (ok) load8<T, V>(rh[u], h, c0, tpr, C);
+            float t[8];
+            weights8<T, V>(t, p.gate == nullptr ? nullptr : static_cast<const T*>(p.gate) + row * C,
+                           1.0f, c0, tpr, C);
+            weights8<T, V>(g[u], static_cast<const T*>(p.post_w), 1.0f, c0, tpr, C);
+            weights8<T, V>(gb[u], static_cast<const T*>(p.post_bias), 0.0f, c0, tpr, C);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                t[i] *= p.scale;
+                g[u][i] *= t[i];
+                gb[u][i] *= t[i];
+            }
+        }
+        gate_row = row;
+    };
+    if (p.y != nullptr)
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            weights8<T, V>(w[u], static_cast<const T*>(p.pre_w), 1.0f, unit_c0<V>(u, lane, tpr),
+                           tpr, C);
+            weights8<T, V>(wb[u], static_cast<const T*>(p.pre_bias), 0.0f,
+                           unit_c0<V>(u, lane, tpr), tpr, C);
+        }
+    auto load = [&](long long row, Raw8<T, V> (&rh)[NU], Raw8<T, V> (&rb)[NU]) {
+        const bool ok = row < p.rows &&
+                        in_bounds(&g_block_status, h + row * C, (long long)C * sizeof(T), p.h, tensor);
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            const int c0 = unit_c0<V>(u, lane, tpr);
+            if (ok) load8<T, V>(rh[u], h + row * C, c0, tpr, C);
             else zero8<T, V>(rh[u]);
-            if (p.b != nullptr) {
-                if (ok) load8<T, V>(rb[u], static_cast<const T*>(p.b) + at, c0, tpr, C);
+            if constexpr (kB) {
+                if (ok) load8<T, V>(rb[u], b + row * C, c0, tpr, C);
                 else zero8<T, V>(rb[u]);
             }
         }
+    };
+    long long row = blockIdx.x;
+    Raw8<T, V> rh[NU], rb[NU];
+    load(row, rh, rb);
+    for (; row < p.rows; row += stride) {
+        Raw8<T, V> nh[NU], nb[NU];
+        load(row + stride, nh, nb);
+        constexpr bool ok = true;
+        const long long at = row * C;
         float v[NU][8];
 #pragma unroll
         for (int u = 0; u < NU; ++u) unpack8<T, V>(rh[u], v[u]);
-        if (p.b != nullptr) {
+        if constexpr (kB) {
+            const long long gr = p.gate != nullptr ? row / p.gate_rows : 0;
+            if (gr != gate_row) gates(gr);
             float m[NU][8];
 #pragma unroll
             for (int u = 0; u < NU; ++u) unpack8<T, V>(rb[u], m[u]);
             if (p.post != kNormNone)
                 normalise<V, TPR, NU>(m, p.post, lane, tpr, C, p.eps, p.inv_c, red, turn);
-            const T* gate = p.gate == nullptr || !valid
-                                ? static_cast<const T*>(p.gate)
-                                : static_cast<const T*>(p.gate) + row / p.gate_rows * C;
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
                 const int c0 = unit_c0<V>(u, lane, tpr);
-                affine8<T, V>(m[u], static_cast<const T*>(p.post_w),
-                              static_cast<const T*>(p.post_bias), c0, tpr, C);
-                affine8<T, V>(m[u], gate, nullptr, c0, tpr, C);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] = fmaf(p.scale, m[u][i], v[u][i]);
+                for (int i = 0; i < 8; ++i) v[u][i] += fmaf(m[u][i], g[u][i], gb[u][i]);
                 const Raw8<T, V> r = pack8<T, V>(v[u]);
                 if (ok) store8<T, V>(r, static_cast<T*>(p.h_out) + at, c0, tpr, C);
                 unpack8<T, V>(r, v[u]);  // the stored value is what the norm reads
@@ -202,165 +233,32 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_fwd_kernel(const __gri
             normalise<V, TPR, NU>(v, p.pre, lane, tpr, C, p.eps, p.inv_c, red, turn);
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
-                const int c0 = unit_c0<V>(u, lane, tpr);
-                affine8<T, V>(v[u], static_cast<const T*>(p.pre_w),
-                              static_cast<const T*>(p.pre_bias), c0, tpr, C);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] = act_of<T>(v[u][i], p.act);
-                if (ok) store8<T, V>(pack8<T, V>(v[u]), static_cast<T*>(p.y) + at, c0, tpr, C);
+                for (int i = 0; i < 8; ++i) v[u][i] = fmaf(v[u][i], w[u][i], wb[u][i]);
+                if (p.act != kActNone)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[u][i] = act_of<T>(v[u][i], p.act);
+                if (ok)
+                    store8<T, V>(pack8<T, V>(v[u]), static_cast<T*>(p.y) + at,
+                                 unit_c0<V>(u, lane, tpr), tpr, C);
             }
+        }
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            rh[u] = nh[u];
+            if constexpr (kB) rb[u] = nb[u];
         }
     }
 }
 
-// Gradients of the rows, and the column sums over this block's rows: block
-// (group, j) takes every blocks_per_group-th step of the group's rows, from
-// its j-th.  kBias: the sums of du and G are wanted too (a bias is there).
-template <typename T, bool V, int TPR, int NU, bool kBias>
-__global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(const __grid_constant__ NormBwd p) {
-    __shared__ float red[2][4][32];
-    extern __shared__ float colbuf[];  // TPR > 0: [warps][C] for the block's column sums
-    int turn = 0;
-    constexpr int kQ = kBias ? 4 : 2;
-    const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
-    const int lane = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % tpr;
-    const int rpb = (int)blockDim.x / tpr;
-    const int C = p.C;
-    const long long tensor = p.rows * C * (long long)sizeof(T);
-    float acc[kQ][NU][8];
-#pragma unroll
-    for (int q = 0; q < kQ; ++q)
-#pragma unroll
-        for (int u = 0; u < NU; ++u)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[q][u][i] = 0.0f;
-    const long long group = blockIdx.x / p.blocks_per_group;
-    const int part_of = (int)(blockIdx.x % p.blocks_per_group);
-    const long long row0 = group * p.group_rows, row1 = row0 + p.group_rows;
-    const T* gate = p.gate == nullptr ? nullptr : static_cast<const T*>(p.gate) + group * C;
-    const T* pre_w = static_cast<const T*>(p.pre_w);
-    const T* pre_bias = static_cast<const T*>(p.pre_bias);
-    const T* post_w = static_cast<const T*>(p.post_w);
-    for (long long base = row0 + (long long)part_of * rpb; base < row1;
-         base += (long long)p.blocks_per_group * rpb) {
-        const long long row = base + (int)threadIdx.x / tpr;
-        const bool valid = row < row1;
-        const long long at = (valid ? row : row0) * C;
-        const T* h = static_cast<const T*>(p.h) + at;
-        const bool ok = valid && in_bounds(&g_block_status, h, (long long)C * sizeof(T), p.h, tensor);
-        // every load of the row is issued before the first of them is used
-        Raw8<T, V> rh[NU], ry[NU], rg[NU], rb[NU];
-#pragma unroll
-        for (int u = 0; u < NU; ++u) {
-            const int c0 = unit_c0<V>(u, lane, tpr);
-            zero8<T, V>(rh[u]); zero8<T, V>(ry[u]); zero8<T, V>(rg[u]); zero8<T, V>(rb[u]);
-            if (ok) {
-                if (p.dy != nullptr) {
-                    load8<T, V>(rh[u], h, c0, tpr, C);
-                    load8<T, V>(ry[u], static_cast<const T*>(p.dy) + at, c0, tpr, C);
-                }
-                if (p.dh_out != nullptr)
-                    load8<T, V>(rg[u], static_cast<const T*>(p.dh_out) + at, c0, tpr, C);
-                if (p.b != nullptr)
-                    load8<T, V>(rb[u], static_cast<const T*>(p.b) + at, c0, tpr, C);
-            }
-        }
-        float G[NU][8];
-#pragma unroll
-        for (int u = 0; u < NU; ++u) unpack8<T, V>(rg[u], G[u]);
-        if (p.dy != nullptr) {
-            float n[NU][8], d[NU][8];
-#pragma unroll
-            for (int u = 0; u < NU; ++u) unpack8<T, V>(rh[u], n[u]);
-            const float rstd =
-                normalise<V, TPR, NU>(n, p.pre, lane, tpr, C, p.eps, p.inv_c, red, turn);
-            float s[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                const int c0 = unit_c0<V>(u, lane, tpr);
-                unpack8<T, V>(ry[u], d[u]);
-                if (p.act != kActNone) {
-                    float a[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) a[i] = n[u][i];
-                    affine8<T, V>(a, pre_w, pre_bias, c0, tpr, C);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) d[u][i] *= act_grad_of<T>(a[i], p.act);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    acc[0][u][i] = fmaf(d[u][i], n[u][i], acc[0][u][i]);
-                    if constexpr (kBias) acc[2][u][i] += d[u][i];
-                }
-                affine8<T, V>(d[u], pre_w, nullptr, c0, tpr, C);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s[0] = fmaf(d[u][i], n[u][i], s[0]);
-                    s[1] += d[u][i];
-                }
-            }
-            row_sum<TPR, 2>(s, red, turn);
-            const float a = s[0] * p.inv_c, b = p.pre == kNormLayer ? s[1] * p.inv_c : 0.0f;
-#pragma unroll
-            for (int u = 0; u < NU; ++u)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    G[u][i] += rstd * (d[u][i] - b - n[u][i] * a);
-        }
-        if (p.dh != nullptr)
-#pragma unroll
-            for (int u = 0; u < NU; ++u)
-                if (ok)
-                    store8<T, V>(pack8<T, V>(G[u]), static_cast<T*>(p.dh) + at,
-                                 unit_c0<V>(u, lane, tpr), tpr, C);
-        if (p.b != nullptr) {
-            float m[NU][8];
-#pragma unroll
-            for (int u = 0; u < NU; ++u) unpack8<T, V>(rb[u], m[u]);
-            float rstd = 1.0f;
-            if (p.post != kNormNone)
-                rstd = normalise<V, TPR, NU>(m, p.post, lane, tpr, C, p.eps, p.inv_c, red, turn);
-            float s[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                const int c0 = unit_c0<V>(u, lane, tpr);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (!ok || (V ? c0 : c0 + i * tpr) >= C) G[u][i] = 0.0f;
-                    acc[1][u][i] = fmaf(G[u][i], m[u][i], acc[1][u][i]);
-                    if constexpr (kBias) acc[3][u][i] += G[u][i];
-                    G[u][i] *= p.scale;
-                }
-                affine8<T, V>(G[u], gate, nullptr, c0, tpr, C);
-                affine8<T, V>(G[u], post_w, nullptr, c0, tpr, C);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s[0] = fmaf(G[u][i], m[u][i], s[0]);
-                    s[1] += G[u][i];
-                }
-            }
-            if (p.db != nullptr) {
-                if (p.post != kNormNone) {
-                    row_sum<TPR, 2>(s, red, turn);
-                    const float a = s[0] * p.inv_c;
-                    const float b = p.post == kNormLayer ? s[1] * p.inv_c : 0.0f;
-#pragma unroll
-                    for (int u = 0; u < NU; ++u)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            G[u][i] = rstd * (G[u][i] - b - m[u][i] * a);
-                }
-#pragma unroll
-                for (int u = 0; u < NU; ++u)
-                    if (ok)
-                        store8<T, V>(pack8<T, V>(G[u]), static_cast<T*>(p.db) + at,
-                                     unit_c0<V>(u, lane, tpr), tpr, C);
-            }
-        }
-    }
-    // ---- this block's column sums -> its slot of the partials
+// A block's column sums -> its slot of the partials.  colbuf (TPR > 0): [warps][C].
+template <bool V, int TPR, int NU, int kQ>
+__device__ __forceinline__ void store_colsums(const NormBwd& p, const float (&acc)[kQ][NU][8],
+                                              int lane, int tpr, float* colbuf) {
     if (p.part == nullptr) return;
+    const int C = p.C;
     const long long part_bytes = (long long)kQ * p.slots * C * 4;
+#pragma unroll
     for (int q = 0; q < kQ; ++q) {
         float* out = p.part + ((long long)q * p.slots + blockIdx.x) * C;
         const bool fits = in_bounds(&g_block_status, out, (long long)C * 4, p.part, part_bytes);
@@ -370,10 +268,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(const __gri
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int c0 = unit_c0<V>(u, lane, tpr), c = V ? c0 + i : c0 + i * tpr;
-                    float a = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < kQ; ++k) a = k == q ? acc[k][u][i] : a;
-                    if (c < C && fits) out[c] = a;
+                    if (c < C && fits) out[c] = acc[q][u][i];
                 }
         } else {
             // rows of one warp by shuffles, then the warps through shared memory
@@ -383,9 +278,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(const __gri
             for (int u = 0; u < NU; ++u)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    float a = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < kQ; ++k) a = k == q ? acc[k][u][i] : a;
+                    float a = acc[q][u][i];
 #pragma unroll
                     for (int o = 16; o >= TPR; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
                     const int c0 = unit_c0<V>(u, lane, tpr), c = V ? c0 + i : c0 + i * tpr;
@@ -399,6 +292,635 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(const __gri
             }
         }
     }
+}
+
+// Gradients of the rows, and the column sums over this block's rows: block
+// (group, j) takes every blocks_per_group-th step of the group's rows, from
+// its j-th.  kGen: a layer norm or a bias is there (row means, sums of du and
+// G); without it the RMS-only arithmetic is a third shorter.
+template <typename T, bool V, int NU, bool kGen>
+__global__ void __launch_bounds__(512) norm_bwd_rows(
+    const __grid_constant__ NormBwd p) {
+    __shared__ float red[2][4][32];
+    int turn = 0;
+    constexpr int kQ = kGen ? 4 : 2;
+    constexpr int TPR = 0;
+    const int tpr = (int)blockDim.x, lane = (int)threadIdx.x;
+    const int C = p.C;
+    const long long tensor = p.rows * C * (long long)sizeof(T);
+    float acc[kQ][NU][8] = {};
+    const long long group = blockIdx.x / p.blocks_per_group;
+    const int part_of = (int)(blockIdx.x % p.blocks_per_group);
+    const long long row0 = group * p.group_rows, row1 = row0 + p.group_rows;
+    const bool has_pre = p.dy != nullptr, has_b = p.b != nullptr;
+    float w[NU][8], wb[NU][8], g[NU][8];  // pre_w, pre_bias, scale * gate * post_w
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+        const int c0 = unit_c0<V>(u, lane, tpr);
+        weights8<T, V>(w[u], static_cast<const T*>(p.pre_w), 1.0f, c0, tpr, C);
+        if constexpr (kGen)
+            weights8<T, V>(wb[u], static_cast<const T*>(p.pre_bias), 0.0f, c0, tpr, C);
+        float t[8];
+        weights8<T, V>(t, p.gate == nullptr ? nullptr : static_cast<const T*>(p.gate) + group * C,
+                       1.0f, c0, tpr, C);
+        weights8<T, V>(g[u], static_cast<const T*>(p.post_w), 1.0f, c0, tpr, C);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[u][i] *= p.scale * t[i];
+    }
+    struct Row {
+        Raw8<T, V> h[NU], y[NU], g[NU], b[NU];
+    };
+    auto load = [&](long long row, Row& r) {
+        const long long at = row * C;
+        const bool ok = row < row1 && in_bounds(&g_block_status, static_cast<const T*>(p.h) + at,
+                                                (long long)C * sizeof(T), p.h, tensor);
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            const int c0 = unit_c0<V>(u, lane, tpr);
+            zero8<T, V>(r.h[u]); zero8<T, V>(r.y[u]); zero8<T, V>(r.g[u]); zero8<T, V>(r.b[u]);
+            if (!ok) continue;
+            if (has_pre) {
+                load8<T, V>(r.h[u], static_cast<const T*>(p.h) + at, c0, tpr, C);
+                load8<T, V>(r.y[u], static_cast<const T*>(p.dy) + at, c0, tpr, C);
+            }
+            if (p.dh_out != nullptr)
+                load8<T, V>(r.g[u], static_cast<const T*>(p.dh_out) + at, c0, tpr, C);
+            if (has_b) load8<T, V>(r.b[u], static_cast<const T*>(p.b) + at, c0, tpr, C);
+        }
+    };
+    const long long stride = p.blocks_per_group;
+    long long row = row0 + part_of;
+    Row cur;
+    load(row, cur);
+    for (; row < row1; row += stride) {
+        Row next;
+        load(row + stride, next);
+        constexpr bool ok = true;
+        const long long at = row * C;
+        float G[NU][8];
+#pragma unroll
+        for (int u = 0; u < NU; ++u) unpack8<T, V>(cur.g[u], G[u]);
+        if (has_pre) {
+            float n[NU][8], d[NU][8];
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                unpack8<T, V>(cur.h[u], n[u]);
+                unpack8<T, V>(cur.y[u], d[u]);
+            }
+            const float rstd = normalise<V, TPR, NU>(n, kGen ? p.pre : kNormRms, lane, tpr, C,
+                                                     p.eps, p.inv_c, red, turn);
+            float s[kGen ? 2 : 1] = {};
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                if (p.act == kActSilu) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        d[u][i] *= act_grad_of<T>(kGen ? fmaf(n[u][i], w[u][i], wb[u][i])
+                                                       : n[u][i] * w[u][i], kActSilu);
+                } else if (p.act == kActGelu) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        d[u][i] *= act_grad_of<T>(kGen ? fmaf(n[u][i], w[u][i], wb[u][i])
+                                                       : n[u][i] * w[u][i], kActGelu);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    acc[0][u][i] = fmaf(d[u][i], n[u][i], acc[0][u][i]);
+                    if constexpr (kGen) acc[2][u][i] += d[u][i];
+                    d[u][i] *= w[u][i];
+                    s[0] = fmaf(d[u][i], n[u][i], s[0]);
+                    if constexpr (kGen) s[1] += d[u][i];
+                }
+            }
+            row_sum<TPR, kGen ? 2 : 1>(s, red, turn);
+            const float a = -s[0] * p.inv_c;
+            float mean = 0.0f;
+            if constexpr (kGen) mean = p.pre == kNormLayer ? s[1] * p.inv_c : 0.0f;
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    G[u][i] = fmaf(rstd, fmaf(n[u][i], a, kGen ? d[u][i] - mean : d[u][i]), G[u][i]);
+        }
+        if (p.dh != nullptr && ok)
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+                store8<T, V>(pack8<T, V>(G[u]), static_cast<T*>(p.dh) + at,
+                             unit_c0<V>(u, lane, tpr), tpr, C);
+        if (has_b) {
+            float m[NU][8];
+#pragma unroll
+            for (int u = 0; u < NU; ++u) unpack8<T, V>(cur.b[u], m[u]);
+            float rstd = 1.0f;
+            if (p.post != kNormNone)
+                rstd = normalise<V, TPR, NU>(m, kGen ? p.post : kNormRms, lane, tpr, C, p.eps,
+                                             p.inv_c, red, turn);
+            float s[kGen ? 2 : 1] = {};
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    acc[1][u][i] = fmaf(G[u][i], m[u][i], acc[1][u][i]);
+                    // (past C, G may hold a row's mean: m and g are 0 there, and the
+                    // sums of those columns are not written)
+                    if constexpr (kGen) acc[3][u][i] += G[u][i];
+                    G[u][i] *= g[u][i];
+                    s[0] = fmaf(G[u][i], m[u][i], s[0]);
+                    if constexpr (kGen) s[1] += G[u][i];
+                }
+            if (p.db != nullptr) {
+                if (p.post != kNormNone) {
+                    row_sum<TPR, kGen ? 2 : 1>(s, red, turn);
+                    const float a = -s[0] * p.inv_c;
+                    float mean = 0.0f;
+                    if constexpr (kGen) mean = p.post == kNormLayer ? s[1] * p.inv_c : 0.0f;
+#pragma unroll
+                    for (int u = 0; u < NU; ++u)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            G[u][i] = rstd * fmaf(m[u][i], a, kGen ? G[u][i] - mean : G[u][i]);
+                }
+                if (ok)
+#pragma unroll
+                    for (int u = 0; u < NU; ++u)
+                        store8<T, V>(pack8<T, V>(G[u]), static_cast<T*>(p.db) + at,
+                                     unit_c0<V>(u, lane, tpr), tpr, C);
+            }
+        }
+        cur = next;
+    }
+    store_colsums<V, TPR, NU, kQ>(p, acc, lane, tpr, nullptr);
+}
+
+// ------------------------------------------------- rows within a warp's share
+constexpr int kTileThreads = 256;  // at most
+
+// Tiles of rows in shared memory.  A tile's bytes start at the 16-byte
+// boundary at or before its first row; what a bulk copy cannot take at a
+// tensor's very end (under 16 bytes) is copied by the threads.
+struct TileShape {
+    int rows;        // rows of a tile
+    int cap;         // bytes of a tile and tensor in shared memory
+    int stages, vec_len;  // vec_len: channels the block's threads cover, the vectors' length
+};
+
+__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes,
+                                         uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar) : "memory");
+}
+
+struct TileSpan {
+    long long from;  // byte of the tensor the copy starts at (a multiple of 16)
+    int off;         // of the tile's first row in the copy
+    int bulk, tail;  // bytes copied in bulk, bytes after them
+};
+__device__ __forceinline__ TileSpan tile_span(long long row0, long long row1, int row_bytes,
+                                              long long tensor) {
+    TileSpan t;
+    const long long b0 = row0 * row_bytes, b1 = row1 * row_bytes;
+    t.from = b0 & ~15LL;
+    t.off = (int)(b0 - t.from);
+    const long long end = (b1 + 15) & ~15LL;
+    t.bulk = (int)((end <= tensor ? end : b1 & ~15LL) - t.from);
+    t.tail = (int)(b1 - t.from) - t.bulk;
+    if (t.tail < 0) t.tail = 0;
+    return t;
+}
+
+// Start the copies of a tile's nT tensors (one thread).
+template <int nT>
+__device__ __forceinline__ void tile_issue(const TileSpan& t, const void* const (&src)[nT],
+                                           uint8_t* stage, int cap, uint32_t bar,
+                                           long long tensor) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < nT; ++k) n += src[k] != nullptr;
+    mbar_arrive_expect_tx(bar, (uint32_t)(n * t.bulk));
+    if (t.bulk == 0) return;
+#pragma unroll
+    for (int k = 0; k < nT; ++k) {
+        if (src[k] == nullptr) continue;
+        const uint8_t* from = static_cast<const uint8_t*>(src[k]) + t.from;
+        // checked build: a range outside the tensor is recorded and read from its start
+        if (!in_bounds(&g_block_status, from, t.bulk, src[k], tensor))
+            from = static_cast<const uint8_t*>(src[k]);
+        bulk_g2s(smem_u32(stage + (size_t)k * cap), from, (uint32_t)t.bulk, bar);
+    }
+}
+// The bytes after the bulk copies (all threads; uniform).
+template <int nT>
+__device__ __forceinline__ void tile_tail(const TileSpan& t, const void* const (&src)[nT],
+                                          uint8_t* stage, int cap) {
+    if (t.tail == 0) return;
+    if ((int)threadIdx.x < t.tail)
+#pragma unroll
+        for (int k = 0; k < nT; ++k)
+            if (src[k] != nullptr)
+                stage[(size_t)k * cap + t.bulk + threadIdx.x] =
+                    static_cast<const uint8_t*>(src[k])[t.from + t.bulk + threadIdx.x];
+    __syncthreads();
+}
+
+// Eight channels of a vector kept in shared memory, as pairs.
+__device__ __forceinline__ void vec8(f2 (&f)[4], const float* s, bool vec, int c0, int step) {
+    if (vec) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(s + c0);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(s + c0 + 4);
+        f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = f2_make(s[c0 + 2 * i * step], s[c0 + (2 * i + 1) * step]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float vec_at(const void* p, int c, int C, float otherwise) {
+    return c >= C ? 0.0f : (p == nullptr ? otherwise : (float)static_cast<const T*>(p)[c]);
+}
+
+// Unit u of a staged row, in registers (zeros for a row that is not there).
+template <typename T, bool V, int TPR>
+__device__ __forceinline__ void tile_unit(f2 (&v)[4], const uint8_t* at, int u, int lane, int C,
+                                          bool ok) {
+    Raw8<T, V> r;
+    if (ok) load8<T, V>(r, reinterpret_cast<const T*>(at), unit_c0<V>(u, lane, TPR), TPR, C);
+    else zero8<T, V>(r);
+    unpack8<T, V>(r, v);
+}
+
+// normalise() on pairs, within a warp's share.
+template <bool V, int TPR, int NU>
+__device__ __forceinline__ float normalise2(f2 (&v)[NU][4], int kind, int lane, int C, float eps,
+                                            float inv_c) {
+    int turn = 0;
+    if (kind == kNormLayer) {
+        f2 t = f2_all(0.0f);
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t = f2_add(t, v[u][i]);
+        float s[1] = {f2_sum(t)};
+        row_sum<TPR, 1>(s, nullptr, turn);
+        const f2 mu = f2_all(-s[0] * inv_c);
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            const int c0 = unit_c0<V>(u, lane, TPR);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[u][i] = f2_add(v[u][i], mu);
+                if constexpr (V) {
+                    if (c0 >= C) v[u][i] = f2_all(0.0f);
+                } else {
+                    float a, b;
+                    f2_get(v[u][i], a, b);
+                    v[u][i] = f2_make(c0 + 2 * i * TPR < C ? a : 0.0f,
+                                      c0 + (2 * i + 1) * TPR < C ? b : 0.0f);
+                }
+            }
+        }
+    }
+    f2 t = f2_all(0.0f);
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = f2_fma(v[u][i], v[u][i], t);
+    float q[1] = {f2_sum(t)};
+    row_sum<TPR, 1>(q, nullptr, turn);
+    const float rstd = 1.0f / sqrtf(fmaf(q[0], inv_c, eps));
+    const f2 r2 = f2_all(rstd);
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] = f2_mul(v[u][i], r2);
+    return rstd;
+}
+
+template <typename T, bool V, int TPR, int NU, bool kB>
+__global__ void __launch_bounds__(kTileThreads, 3) norm_fwd_tiles(
+    const __grid_constant__ NormFwd p, const __grid_constant__ TileShape sh) {
+    extern __shared__ __align__(128) uint8_t tile_smem[];
+    constexpr int nT = kB ? 2 : 1;
+    const int rpp = (int)blockDim.x / TPR;  // rows a pass
+    const int lane = (int)threadIdx.x % TPR, sub = (int)threadIdx.x / TPR, C = p.C;
+    const int row_bytes = C * (int)sizeof(T);
+    const long long tensor = p.rows * row_bytes;
+    const long long tiles = (p.rows + sh.rows - 1) / sh.rows;
+    uint8_t* ring = tile_smem;
+    const size_t stage_bytes = (size_t)nT * sh.cap;
+    float* vecs = reinterpret_cast<float*>(ring + sh.stages * stage_bytes);  // w, wb, g, gb
+    const int L = sh.vec_len;
+    uint64_t* full = reinterpret_cast<uint64_t*>(vecs + 4 * L);
+    const void* src[nT];
+    src[0] = p.h;
+    if constexpr (kB) src[1] = p.b;
+    auto span = [&](long long t) {
+        const long long r0 = t * sh.rows;
+        return tile_span(r0, min(r0 + sh.rows, p.rows), row_bytes, tensor);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < sh.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        fence_mbar_init();
+        for (int s = 0; s < sh.stages; ++s) {
+            const long long t = blockIdx.x + (long long)s * gridDim.x;
+            if (t < tiles)
+                tile_issue<nT>(span(t), src, ring + s * stage_bytes, sh.cap, smem_u32(&full[s]), tensor);
+        }
+    }
+    for (int c = threadIdx.x; c < L; c += blockDim.x) {
+        vecs[c] = vec_at<T>(p.pre_w, c, C, 1.0f);
+        vecs[L + c] = vec_at<T>(p.pre_bias, c, C, 0.0f);
+        // one gate for all rows: with the scale and the post norm's vectors
+        const float g = p.scale * (p.gate_rows >= p.rows ? vec_at<T>(p.gate, c, C, 1.0f) : 1.0f);
+        vecs[2 * L + c] = g * vec_at<T>(p.post_w, c, C, 1.0f);
+        vecs[3 * L + c] = g * vec_at<T>(p.post_bias, c, C, 0.0f);
+    }
+    __syncthreads();
+    const bool gated = kB && p.gate != nullptr && p.gate_rows < p.rows;
+    const bool post_bias = p.post_bias != nullptr, pre_bias = p.pre_bias != nullptr;
+    int st = 0;
+    uint32_t ph = 0;
+    bool live = true;
+    for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+        if (live && !mbar_wait(smem_u32(&full[st]), ph, &g_block_status, kWaitLimitNs)) live = false;
+        uint8_t* stage = ring + st * stage_bytes;
+        const TileSpan sp = span(t);
+        tile_tail<nT>(sp, src, stage, sh.cap);
+        const int n = (int)min((long long)sh.rows, p.rows - t * sh.rows);
+        for (int r0 = 0; r0 < n; r0 += rpp) {
+            const int r = r0 + sub;
+            const bool ok = live && r < n;
+            const long long row = t * sh.rows + r, at = row * C;
+            const uint8_t* in = stage + sp.off + (size_t)r * row_bytes;
+            f2 v[NU][4];
+#pragma unroll
+            for (int u = 0; u < NU; ++u) tile_unit<T, V, TPR>(v[u], in, u, lane, C, ok);
+            if constexpr (kB) {
+                f2 m[NU][4];
+#pragma unroll
+                for (int u = 0; u < NU; ++u)
+                    tile_unit<T, V, TPR>(m[u], in + sh.cap, u, lane, C, ok);
+                if (p.post != kNormNone)
+                    normalise2<V, TPR, NU>(m, p.post, lane, C, p.eps, p.inv_c);
+                const T* gate = static_cast<const T*>(p.gate) + (gated && ok ? row / p.gate_rows * C : 0);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    const int c0 = unit_c0<V>(u, lane, TPR);
+                    f2 f[4];
+                    vec8(f, vecs + 2 * L, V, c0, TPR);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m[u][i] = f2_mul(m[u][i], f[i]);
+                    if (post_bias) {
+                        vec8(f, vecs + 3 * L, V, c0, TPR);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) m[u][i] = f2_add(m[u][i], f[i]);
+                    }
+                    if (gated) {
+                        Raw8<T, V> r;
+                        load8<T, V>(r, gate, c0, TPR, C);
+                        unpack8<T, V>(r, f);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) m[u][i] = f2_mul(m[u][i], f[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[u][i] = f2_add(v[u][i], m[u][i]);
+                    const Raw8<T, V> o = pack8<T, V>(v[u]);
+                    if (ok) store8<T, V>(o, static_cast<T*>(p.h_out) + at, c0, TPR, C);
+                    unpack8<T, V>(o, v[u]);  // the stored value is what the norm reads
+                }
+            }
+            if (p.y != nullptr) {
+                normalise2<V, TPR, NU>(v, p.pre, lane, C, p.eps, p.inv_c);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    const int c0 = unit_c0<V>(u, lane, TPR);
+                    f2 f[4];
+                    vec8(f, vecs, V, c0, TPR);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[u][i] = f2_mul(v[u][i], f[i]);
+                    if (pre_bias) {
+                        vec8(f, vecs + L, V, c0, TPR);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[u][i] = f2_add(v[u][i], f[i]);
+                    }
+                    if (p.act == kActSilu) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[u][i] = f2_act<T>(v[u][i], kActSilu);
+                    } else if (p.act == kActGelu) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[u][i] = f2_act<T>(v[u][i], kActGelu);
+                    }
+                    if (ok) store8<T, V>(pack8<T, V>(v[u]), static_cast<T*>(p.y) + at, c0, TPR, C);
+                }
+            }
+        }
+        __syncthreads();  // every thread is done with the stage
+        if (threadIdx.x == 0) {
+            const long long nt = t + (long long)sh.stages * gridDim.x;
+            if (nt < tiles)
+                tile_issue<nT>(span(nt), src, stage, sh.cap, smem_u32(&full[st]), tensor);
+        }
+        if (++st == sh.stages) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+}
+
+template <typename T, bool V, int TPR, int NU, bool kGen>
+__global__ void __launch_bounds__(kTileThreads, 2) norm_bwd_tiles(
+    const __grid_constant__ NormBwd p, const __grid_constant__ TileShape sh) {
+    extern __shared__ __align__(128) uint8_t tile_smem[];
+    constexpr int nT = 4, kQ = kGen ? 4 : 2;
+    const int rpp = (int)blockDim.x / TPR;  // rows a pass
+    const int lane = (int)threadIdx.x % TPR, sub = (int)threadIdx.x / TPR, C = p.C;
+    const int row_bytes = C * (int)sizeof(T);
+    const long long tensor = p.rows * row_bytes;
+    const long long group = blockIdx.x / p.blocks_per_group;
+    const int part_of = (int)(blockIdx.x % p.blocks_per_group);
+    const long long row0 = group * p.group_rows, row1 = row0 + p.group_rows;
+    const long long tiles = (p.group_rows + sh.rows - 1) / sh.rows;
+    uint8_t* ring = tile_smem;
+    const size_t stage_bytes = (size_t)nT * sh.cap;
+    float* vecs = reinterpret_cast<float*>(ring + sh.stages * stage_bytes);  // pre_w, pre_bias, g
+    const int L = sh.vec_len;
+    uint64_t* full = reinterpret_cast<uint64_t*>(vecs + 3 * L);
+    const bool has_pre = p.dy != nullptr, has_b = p.b != nullptr;
+    const void* src[nT] = {has_pre ? p.h : nullptr, p.dy, p.dh_out, p.b};
+    auto span = [&](long long t) {
+        const long long r0 = row0 + t * sh.rows;
+        return tile_span(r0, min(r0 + sh.rows, row1), row_bytes, tensor);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < sh.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        fence_mbar_init();
+        for (int s = 0; s < sh.stages; ++s) {
+            const long long t = part_of + (long long)s * p.blocks_per_group;
+            if (t < tiles)
+                tile_issue<nT>(span(t), src, ring + s * stage_bytes, sh.cap, smem_u32(&full[s]), tensor);
+        }
+    }
+    const T* gate = p.gate == nullptr ? nullptr : static_cast<const T*>(p.gate) + group * C;
+    for (int c = threadIdx.x; c < L; c += blockDim.x) {
+        vecs[c] = vec_at<T>(p.pre_w, c, C, 1.0f);
+        vecs[L + c] = vec_at<T>(p.pre_bias, c, C, 0.0f);
+        vecs[2 * L + c] = p.scale * vec_at<T>(gate, c, C, 1.0f) * vec_at<T>(p.post_w, c, C, 1.0f);
+    }
+    __syncthreads();
+    f2 acc[kQ][NU][4];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q)
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[q][u][i] = f2_all(0.0f);
+    int st = 0;
+    uint32_t ph = 0;
+    bool live = true;
+    for (long long t = part_of; t < tiles; t += p.blocks_per_group) {
+        if (live && !mbar_wait(smem_u32(&full[st]), ph, &g_block_status, kWaitLimitNs)) live = false;
+        uint8_t* stage = ring + st * stage_bytes;
+        const TileSpan sp = span(t);
+        tile_tail<nT>(sp, src, stage, sh.cap);
+        const int n = (int)min((long long)sh.rows, p.group_rows - t * sh.rows);
+        for (int r0 = 0; r0 < n; r0 += rpp) {
+            const int r = r0 + sub;
+            const bool ok = live && r < n;
+            const long long at = (row0 + t * sh.rows + r) * C;
+            const uint8_t* in = stage + sp.off + (size_t)r * row_bytes;
+            // two arrays of the row's channels: v is h, then b; G is dy and what
+            // comes of it, then the gradient of the stream and what comes of that
+            f2 v[NU][4], G[NU][4];
+            if (has_pre) {
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    tile_unit<T, V, TPR>(v[u], in, u, lane, C, ok);
+                    tile_unit<T, V, TPR>(G[u], in + sh.cap, u, lane, C, ok);
+                }
+                const float rstd = normalise2<V, TPR, NU>(v, kGen ? p.pre : kNormRms, lane, C,
+                                                          p.eps, p.inv_c);
+                f2 s0 = f2_all(0.0f), s1 = f2_all(0.0f);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    const int c0 = unit_c0<V>(u, lane, TPR);
+                    f2 w[4], wb[4];
+                    vec8(w, vecs, V, c0, TPR);
+                    if constexpr (kGen) vec8(wb, vecs + L, V, c0, TPR);
+                    auto slope = [&](int kind) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const f2 a = kGen ? f2_fma(v[u][i], w[i], wb[i]) : f2_mul(v[u][i], w[i]);
+                            G[u][i] = f2_mul(G[u][i], f2_act_grad<T>(a, kind));
+                        }
+                    };
+                    if (p.act == kActSilu) slope(kActSilu);
+                    else if (p.act == kActGelu) slope(kActGelu);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[0][u][i] = f2_fma(G[u][i], v[u][i], acc[0][u][i]);
+                        if constexpr (kGen) acc[2][u][i] = f2_add(acc[2][u][i], G[u][i]);
+                        G[u][i] = f2_mul(G[u][i], w[i]);
+                        s0 = f2_fma(G[u][i], v[u][i], s0);
+                        if constexpr (kGen) s1 = f2_add(s1, G[u][i]);
+                    }
+                }
+                float s[kGen ? 2 : 1];
+                s[0] = f2_sum(s0);
+                if constexpr (kGen) s[1] = f2_sum(s1);
+                int turn = 0;
+                row_sum<TPR, kGen ? 2 : 1>(s, nullptr, turn);
+                const f2 a = f2_all(-s[0] * p.inv_c), r2 = f2_all(rstd);
+                f2 mean = f2_all(0.0f);
+                if constexpr (kGen) mean = f2_all(p.pre == kNormLayer ? -s[1] * p.inv_c : 0.0f);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    f2 g[4];
+                    tile_unit<T, V, TPR>(g, in + 2 * sh.cap, u, lane, C, ok && p.dh_out != nullptr);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        G[u][i] = f2_fma(r2, f2_fma(v[u][i], a, kGen ? f2_add(G[u][i], mean) : G[u][i]),
+                                         g[i]);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < NU; ++u)
+                    tile_unit<T, V, TPR>(G[u], in + 2 * sh.cap, u, lane, C, ok);
+            }
+            if (p.dh != nullptr && ok)
+#pragma unroll
+                for (int u = 0; u < NU; ++u)
+                    store8<T, V>(pack8<T, V>(G[u]), static_cast<T*>(p.dh) + at,
+                                 unit_c0<V>(u, lane, TPR), TPR, C);
+            if (has_b) {
+#pragma unroll
+                for (int u = 0; u < NU; ++u)
+                    tile_unit<T, V, TPR>(v[u], in + 3 * sh.cap, u, lane, C, ok);
+                float rstd = 1.0f;
+                if (p.post != kNormNone)
+                    rstd = normalise2<V, TPR, NU>(v, kGen ? p.post : kNormRms, lane, C, p.eps,
+                                                  p.inv_c);
+                f2 s0 = f2_all(0.0f), s1 = f2_all(0.0f);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    f2 g[4];
+                    vec8(g, vecs + 2 * L, V, unit_c0<V>(u, lane, TPR), TPR);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[1][u][i] = f2_fma(G[u][i], v[u][i], acc[1][u][i]);
+                        // (past C, G may hold a row's mean: v and g are 0 there, and the
+                        // sums of those columns are not written)
+                        if constexpr (kGen) acc[3][u][i] = f2_add(acc[3][u][i], G[u][i]);
+                        G[u][i] = f2_mul(G[u][i], g[i]);
+                        s0 = f2_fma(G[u][i], v[u][i], s0);
+                        if constexpr (kGen) s1 = f2_add(s1, G[u][i]);
+                    }
+                }
+                if (p.db != nullptr) {
+                    if (p.post != kNormNone) {
+                        float s[kGen ? 2 : 1];
+                        s[0] = f2_sum(s0);
+                        if constexpr (kGen) s[1] = f2_sum(s1);
+                        int turn = 0;
+                        row_sum<TPR, kGen ? 2 : 1>(s, nullptr, turn);
+                        const f2 a = f2_all(-s[0] * p.inv_c), r2 = f2_all(rstd);
+                        f2 mean = f2_all(0.0f);
+                        if constexpr (kGen) mean = f2_all(p.post == kNormLayer ? -s[1] * p.inv_c : 0.0f);
+#pragma unroll
+                        for (int u = 0; u < NU; ++u)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                G[u][i] = f2_mul(r2, f2_fma(v[u][i], a,
+                                                            kGen ? f2_add(G[u][i], mean) : G[u][i]));
+                    }
+                    if (ok)
+#pragma unroll
+                        for (int u = 0; u < NU; ++u)
+                            store8<T, V>(pack8<T, V>(G[u]), static_cast<T*>(p.db) + at,
+                                         unit_c0<V>(u, lane, TPR), TPR, C);
+                }
+            }
+        }
+        __syncthreads();  // every thread is done with the stage
+        if (threadIdx.x == 0) {
+            const long long nt = t + (long long)sh.stages * p.blocks_per_group;
+            if (nt < tiles)
+                tile_issue<nT>(span(nt), src, stage, sh.cap, smem_u32(&full[st]), tensor);
+        }
+        if (++st == sh.stages) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+    float sums[kQ][NU][8];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q)
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f2_get(acc[q][u][i], sums[q][u][2 * i], sums[q][u][2 * i + 1]);
+    // (the ring is idle: every copy was waited for)
+    store_colsums<V, TPR, NU, kQ>(p, sums, lane, TPR, reinterpret_cast<float*>(ring));
 }
 
 struct NormFin {
@@ -422,35 +944,52 @@ __device__ __forceinline__ float get(const void* src, long long i, float otherwi
     return src == nullptr ? otherwise : (float)static_cast<const T*>(src)[i];
 }
 
-// Sum over `n` partial rows, `stride` rows apart, of column c, by the block's
-// 32 rows of threads (threadIdx.y), in a fixed order.
-__device__ __forceinline__ float fin_sum(const float* src, long long n, long long stride, int c,
-                                         int C, float (*buf)[33]) {
-    float a = 0.0f;
-    if (c < C)
-        for (long long i = threadIdx.y; i < n; i += 32) a += src[i * stride * C + c];
+// Sums over `n` partial rows, `stride` rows apart, of column c of the nq
+// quantities: 8 columns a block (few columns leave few blocks, so a block's 128
+// thread rows go down the partials), in a fixed order; every thread of a column
+// has them.
+constexpr int kFinCols = 8, kFinRows = 128;
+__device__ __forceinline__ void fin_sums(const float* src, long long slots, int nq, long long n,
+                                         long long stride, int c, int C, float (&s)[4],
+                                         float (*buf)[32][kFinCols]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s[q] = 0.0f;
+    if (c < C) {
+#pragma unroll 2
+        for (long long i = threadIdx.y; i < n; i += kFinRows)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (q < nq) s[q] += src[(q * slots + i * stride) * C + c];
+    }
+    const int t = threadIdx.y * kFinCols + threadIdx.x;  // a warp: 4 rows of 8 columns
     __syncthreads();
-    buf[threadIdx.y][threadIdx.x] = a;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        s[q] += __shfl_xor_sync(0xffffffffu, s[q], 8);
+        s[q] += __shfl_xor_sync(0xffffffffu, s[q], 16);
+        if ((t & 31) < kFinCols) buf[q][t >> 5][t & 31] = s[q];
+    }
     __syncthreads();
-    a = 0.0f;
-    if (threadIdx.y == 0)
-        for (int i = 0; i < 32; ++i) a += buf[i][threadIdx.x];
-    return a;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        s[q] = 0.0f;
+        if (threadIdx.y == 0)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[q] += buf[q][i][threadIdx.x];
+    }
 }
 
 // Block (column block, gate group): the group's sums over its blocks'
 // partials; dgate; with one group the other parameter gradients too, with
 // several the group's terms of them go to its first slot for the next launch.
 template <typename T>
-__global__ void norm_fin_group_kernel(const __grid_constant__ NormFin p) {
-    __shared__ float buf[32][33];
-    const int c = blockIdx.x * 32 + threadIdx.x, C = p.C;
+__global__ void __launch_bounds__(1024) norm_fin_group_kernel(const __grid_constant__ NormFin p) {
+    __shared__ float buf[4][32][kFinCols];
+    const int c = blockIdx.x * kFinCols + threadIdx.x, C = p.C, nq = p.has_bias ? 4 : 2;
     for (long long g = blockIdx.y; g < p.groups; g += gridDim.y) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        const int nq = p.has_bias ? 4 : 2;
-        for (int q = 0; q < nq; ++q)
-            s[q] = fin_sum(p.part + ((long long)q * p.slots + g * p.blocks_per_group) * C,
-                           p.blocks_per_group, 1, c, C, buf);
+        float s[4];
+        fin_sums(p.part + g * p.blocks_per_group * C, p.slots, nq, p.blocks_per_group, 1, c, C, s,
+                 buf);
         if (threadIdx.y != 0 || c >= C) continue;
         if (p.has_b) {
             const float w = get<T>(p.post_w, c, 1.0f), b = get<T>(p.post_bias, c, 0.0f);
@@ -473,16 +1012,17 @@ __global__ void norm_fin_group_kernel(const __grid_constant__ NormFin p) {
 
 // Several gate groups: the sums of the groups' terms.
 template <typename T>
-__global__ void norm_fin_all_kernel(const __grid_constant__ NormFin p) {
-    __shared__ float buf[32][33];
-    const int c = blockIdx.x * 32 + threadIdx.x, C = p.C;
-    void* dst[4] = {p.dpre_w, p.dpost_w, p.dpre_bias, p.dpost_bias};
-    for (int q = 0; q < (p.has_bias ? 4 : 2); ++q) {
-        if (dst[q] == nullptr) continue;
-        const float s = fin_sum(p.part + (long long)q * p.slots * C, p.groups, p.blocks_per_group,
-                                c, C, buf);
-        if (threadIdx.y == 0 && c < C) put<T>(dst[q], c, s);
-    }
+__global__ void __launch_bounds__(1024) norm_fin_all_kernel(const __grid_constant__ NormFin p) {
+    __shared__ float buf[4][32][kFinCols];
+    const int c = blockIdx.x * kFinCols + threadIdx.x;
+    float s[4];
+    fin_sums(p.part, p.slots, p.has_bias ? 4 : 2, p.groups, p.blocks_per_group, c, p.C, s, buf);
+    if (threadIdx.y != 0 || c >= p.C) return;
+    put<T>(p.dpre_w, c, s[0]);
+    put<T>(p.dpost_w, c, s[1]);
+    if (!p.has_bias) return;
+    put<T>(p.dpre_bias, c, s[2]);
+    put<T>(p.dpost_bias, c, s[3]);
 }
 
 }  // namespace ccv3d

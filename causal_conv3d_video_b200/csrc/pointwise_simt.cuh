@@ -40,101 +40,138 @@ __device__ __forceinline__ void pw_store(const PwOut& o, long long m, int n, flo
     static_cast<T*>(o.out)[at] = (T)u;
 }
 
-constexpr int kPwTile = 128, kPwK = 16, kPwPad = 4;
+constexpr int kPwK = 16, kPwPad = 4;
 
-// Eight operand values of a thread: along k (row r, k0 .. k0 + 7) or along the
-// row index (k, r0 .. r0 + 7).
-template <typename T, bool KMAJOR>
-__device__ __forceinline__ void pw_fetch(float (&v)[8], const T* base, long long s_row,
+// kV operand values of a thread: along k (row r, k0 .. k0 + kV - 1) or along the
+// row index (k, r0 .. ).  R: rows of the tile (256 threads fetch R x 16).
+template <typename T, bool KMAJOR, int R>
+__device__ __forceinline__ void pw_fetch(float (&v)[R / 16], const T* base, long long s_row,
                                          long long s_k, long long row0, long long rows,
                                          long long k0, long long k1, int tid, bool vec) {
-    const long long r = KMAJOR ? row0 + (tid >> 1) : row0 + (tid & 15) * 8;
-    const long long k = KMAJOR ? k0 + (tid & 1) * 8 : k0 + (tid >> 4);
+    constexpr int kV = R / 16, kPer = 16 / kV;  // threads along a row's 16 k
+    const long long r = KMAJOR ? row0 + tid / kPer : row0 + (tid & 15) * kV;
+    const long long k = KMAJOR ? k0 + tid % kPer * kV : k0 + (tid >> 4);
     // (s_row = 1 or s_k = 1 along the contiguous direction)
     const T* p = base + (KMAJOR ? r * s_row + k : k * s_k + r);
-    const bool whole = KMAJOR ? r < rows && k + 8 <= k1 : k < k1 && r + 8 <= rows;
+    const bool whole = KMAJOR ? r < rows && k + kV <= k1 : k < k1 && r + kV <= rows;
     if (whole && vec) {
-        Raw8<T, true> raw;
-        load8<T, true>(raw, p, 0, 1, 8);
-        unpack8<T, true>(raw, v);
+#pragma unroll
+        for (int i = 0; i < kV; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p + i);
+            v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kV; ++i) {
             const bool in = KMAJOR ? r < rows && k + i < k1 : k < k1 && r + i < rows;
             v[i] = in ? (float)p[i] : 0.0f;
         }
     }
 }
 
-template <bool KMAJOR>
-__device__ __forceinline__ void pw_put(float (*s)[kPwTile + kPwPad], const float (&v)[8], int tid) {
+template <bool KMAJOR, int R>
+__device__ __forceinline__ void pw_put(float (*s)[R + kPwPad], const float (&v)[R / 16], int tid) {
+    constexpr int kV = R / 16, kPer = 16 / kV;
     if constexpr (KMAJOR) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[(tid & 1) * 8 + i][tid >> 1] = v[i];
+        for (int i = 0; i < kV; ++i) s[tid % kPer * kV + i][tid / kPer] = v[i];
     } else {
-        float4* d = reinterpret_cast<float4*>(&s[tid >> 4][(tid & 15) * 8]);
-        d[0] = make_float4(v[0], v[1], v[2], v[3]);
-        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+        for (int i = 0; i < kV; i += 4)
+            *reinterpret_cast<float4*>(&s[tid >> 4][(tid & 15) * kV + i]) =
+                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     }
 }
 
-// 128 x 128 tile a block, 8 x 8 values a thread, k in steps of 16 through two
-// shared-memory buffers; the next step's operands wait in registers.
-template <typename T, bool AK, bool BK>
+// S x S tile a block (S = 128 or 64), S/16 x S/16 values a thread, k in steps of
+// 16 through two shared-memory buffers; the next step's operands wait in
+// registers.  128 has the better ratio of FMAs to shared-memory reads; 64 is
+// for products whose edges or few tiles would idle much of it.
+template <typename T, bool AK, bool BK, int S>
 __global__ void __launch_bounds__(256) pw_simt_kernel(const __grid_constant__ PwSimt p) {
-    __shared__ float sa[2][kPwK][kPwTile + kPwPad], sb[2][kPwK][kPwTile + kPwPad];
+    constexpr int kT = S / 16, kH = kT / 4;
+    __shared__ float sa[2][kPwK][S + kPwPad], sb[2][kPwK][S + kPwPad];
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int tiles_n = (p.N + kPwTile - 1) / kPwTile;
+    const int tiles_n = (p.N + S - 1) / S;
     const long long tile = blockIdx.x;
-    const long long m0 = tile / tiles_n * kPwTile;
-    const int n0 = (int)(tile % tiles_n) * kPwTile;
+    const long long m0 = tile / tiles_n * S;
+    const int n0 = (int)(tile % tiles_n) * S;
     const long long kb = (long long)blockIdx.z * p.k_per_split;
     const long long ke = kb + p.k_per_split < p.K ? kb + p.k_per_split : p.K;
     const T *A = static_cast<const T*>(p.A), *B = static_cast<const T*>(p.B);
-    float acc[8][8] = {}, va[8], vb[8];
-    pw_fetch<T, AK>(va, A, p.sam, p.sak, m0, p.M, kb, ke, tid, p.vec);
-    pw_fetch<T, BK>(vb, B, p.sbn, p.sbk, n0, p.N, kb, ke, tid, p.vec);
+    float acc[kT][kT] = {}, va[kT], vb[kT];
+    pw_fetch<T, AK, S>(va, A, p.sam, p.sak, m0, p.M, kb, ke, tid, p.vec);
+    pw_fetch<T, BK, S>(vb, B, p.sbn, p.sbk, n0, p.N, kb, ke, tid, p.vec);
     int cur = 0;
     for (long long k = kb; k < ke; k += kPwK, cur ^= 1) {
-        pw_put<AK>(sa[cur], va, tid);
-        pw_put<BK>(sb[cur], vb, tid);
+        pw_put<AK, S>(sa[cur], va, tid);
+        pw_put<BK, S>(sb[cur], vb, tid);
         __syncthreads();
         if (k + kPwK < ke) {
-            pw_fetch<T, AK>(va, A, p.sam, p.sak, m0, p.M, k + kPwK, ke, tid, p.vec);
-            pw_fetch<T, BK>(vb, B, p.sbn, p.sbk, n0, p.N, k + kPwK, ke, tid, p.vec);
+            pw_fetch<T, AK, S>(va, A, p.sam, p.sak, m0, p.M, k + kPwK, ke, tid, p.vec);
+            pw_fetch<T, BK, S>(vb, B, p.sbn, p.sbk, n0, p.N, k + kPwK, ke, tid, p.vec);
         }
 #pragma unroll
         for (int kk = 0; kk < kPwK; ++kk) {
-            float a[8], b[8];
+            float a[kT], b[kT];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < kH; ++h) {
                 const float4 x = *reinterpret_cast<const float4*>(&sa[cur][kk][h * 64 + ty * 4]);
                 const float4 y = *reinterpret_cast<const float4*>(&sb[cur][kk][h * 64 + tx * 4]);
                 a[h * 4] = x.x; a[h * 4 + 1] = x.y; a[h * 4 + 2] = x.z; a[h * 4 + 3] = x.w;
                 b[h * 4] = y.x; b[h * 4 + 1] = y.y; b[h * 4 + 2] = y.z; b[h * 4 + 3] = y.w;
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < kT; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < kT; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
         }
         // (one barrier a step: the next step writes the other buffer, whose
         // readers passed this step's barrier)
     }
+    // Epilogue: everything is read before the first store (out may be the
+    // residual, so the compiler keeps a load after a store where it stands:
+    // one by one, 64 residual loads waited out 64 memory latencies).
+    const PwOut& o = p.o;
+    auto row = [&](int i) { return m0 + (i >> 2) * 64 + ty * 4 + (i & 3); };
+    auto col = [&](int j) { return n0 + (j >> 2) * 64 + tx * 4 + (j & 3); };
+    if (o.partial != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const long long m = m0 + (i >> 2) * 64 + ty * 4 + (i & 3);
-        if (m >= p.M) continue;
+        for (int i = 0; i < kT; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int n = n0 + (j >> 2) * 64 + tx * 4 + (j & 3);
-            if (n >= p.N) continue;
-            if (p.o.partial != nullptr)
-                p.o.partial[((long long)blockIdx.z * p.M + m) * p.N + n] = acc[i][j];
-            else
-                pw_store<T>(p.o, m, n, acc[i][j]);
-        }
+            for (int j = 0; j < kT; ++j)
+                if (row(i) < p.M && col(j) < p.N)
+                    o.partial[((long long)blockIdx.z * p.M + row(i)) * p.N + col(j)] = acc[i][j];
+        return;
     }
+    const T *bias = static_cast<const T*>(o.bias), *residual = static_cast<const T*>(o.residual);
+    float res[kT][kT];
+    if (residual != nullptr)
+#pragma unroll
+        for (int i = 0; i < kT; ++i)
+#pragma unroll
+            for (int j = 0; j < kT; ++j)
+                res[i][j] = row(i) < p.M && col(j) < p.N ? (float)residual[row(i) * o.N + col(j)] : 0.0f;
+    if (bias != nullptr)
+#pragma unroll
+        for (int j = 0; j < kT; ++j) {
+            const float b = col(j) < p.N ? (float)bias[col(j)] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kT; ++i) acc[i][j] += b;
+        }
+    const long long bytes = o.M * o.N * (long long)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kT; ++i)
+#pragma unroll
+        for (int j = 0; j < kT; ++j) {
+            if (row(i) >= p.M || col(j) >= p.N) continue;
+            T* out = static_cast<T*>(o.out) + row(i) * o.N + col(j);
+            if (!in_bounds(&g_block_status, out, sizeof(T), o.out, bytes)) continue;
+            if (o.pre != nullptr) static_cast<T*>(o.pre)[row(i) * o.N + col(j)] = (T)acc[i][j];
+            float u = act_of<T>(acc[i][j], o.act);
+            if (residual != nullptr) u += res[i][j];
+            *out = (T)u;
+        }
 }
 
 // The partials of a split reduction, added in order, through the epilogue.
@@ -218,20 +255,35 @@ __global__ void __launch_bounds__(256) pw_dact_kernel(const T* pre, const T* dou
     const long long r0 = (long long)blockIdx.y * chunk;
     const long long r1 = r0 + chunk < M ? r0 + chunk : M;
     float acc[8] = {};
-    for (long long r = r0 + sub; r < r1; r += rows) {
-        Raw8<T, V> rd, rp;
-        float d[8], u[8];
-        load8<T, V>(rd, dout + r * N, c0, tpr, N);
-        if (pre != nullptr) load8<T, V>(rp, pre + r * N, c0, tpr, N);
-        unpack8<T, V>(rd, d);
-        if (pre != nullptr) {
-            unpack8<T, V>(rp, u);
+    // four rows at a time, all loads before the stores (dp could be any memory
+    // to the compiler, which would not move a load before a store)
+    constexpr int kU = 4;
+    for (long long r = r0 + sub; r < r1; r += (long long)kU * rows) {
+        Raw8<T, V> rd[kU], rp[kU];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] *= act_grad_of<T>(u[i], act);
+        for (int j = 0; j < kU; ++j) {
+            const long long at = r + (long long)j * rows;
+            zero8<T, V>(rd[j]);
+            zero8<T, V>(rp[j]);
+            if (at < r1) {
+                load8<T, V>(rd[j], dout + at * N, c0, tpr, N);
+                if (pre != nullptr) load8<T, V>(rp[j], pre + at * N, c0, tpr, N);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += d[i];
-        if (dp != nullptr) store8<T, V>(pack8<T, V>(d), dp + r * ldp, c0, tpr, ldp);
+        for (int j = 0; j < kU; ++j) {
+            const long long at = r + (long long)j * rows;
+            float d[8], u[8];
+            unpack8<T, V>(rd[j], d);
+            if (pre != nullptr) {
+                unpack8<T, V>(rp[j], u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] *= act_grad_of<T>(u[i], act);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] += d[i];
+            if (dp != nullptr && at < r1) store8<T, V>(pack8<T, V>(d), dp + at * ldp, c0, tpr, ldp);
+        }
     }
     if (colsum == nullptr) return;
 #pragma unroll

@@ -13,7 +13,10 @@
 // HBM-bound: e + 1 + 1/32 (8 bits) or e + 1/2 + 1/32 bytes a channel in each
 // direction, e = 2 or 4.  A group is four threads of eight channels, its
 // maximum two shuffles.  Frames are the grid's second axis, so a ring slot is
-// found once per block.
+// found once per block.  Each thread moves kQUnits units of eight channels a
+// block stride apart, all their loads before the first store.  Where C is a
+// multiple of 32 (kFlat) a frame is one run of groups and a unit's places need
+// no division by the channel count.
 #pragma once
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
@@ -109,10 +112,20 @@ __device__ __forceinline__ void decode8(uint2 w, int c, int fmt, float (&x)[8]) 
     for (int i = 0; i < 8; ++i) x[i] *= k;
 }
 
-// blockIdx.y = n * frames + i; V: the channel count is a multiple of 8.
-template <typename T, bool V>
-__global__ void __launch_bounds__(256) qcache_write_kernel(const __grid_constant__ QCacheJob p,
-                                                           int fmt) {
+constexpr int kQUnits = 4;
+constexpr int kQThreads = 256;
+
+// Where unit u of a frame lies: its pixel, eight-channel unit of the pixel.
+struct QPlace {
+    long long px;
+    int r;
+};
+
+// blockIdx.y = n * frames + i; V: the channel count is a multiple of 8, kFlat:
+// of 32.
+template <typename T, bool V, bool kFlat>
+__global__ void __launch_bounds__(kQThreads) qcache_write_kernel(const __grid_constant__ QCacheJob p,
+                                                                 int fmt) {
     const int n = blockIdx.y / p.frames, i = blockIdx.y - n * p.frames;
     const long long slot = (long long)n * p.slots + (p.slot + i) % p.slots;
     const T* src = static_cast<const T*>(p.src) +
@@ -122,52 +135,64 @@ __global__ void __launch_bounds__(256) qcache_write_kernel(const __grid_constant
     const long long x_bytes = (long long)p.N * p.T * p.pixels * p.C * (long long)sizeof(T);
     const long long s_bytes = (long long)p.N * p.slots * p.pixels * p.groups;
     const int per = p.groups * 4;  // threads a pixel
-    const long long units = p.pixels * per, step = (long long)gridDim.x * blockDim.x;
-    // whole warps stay in the loop together: a group's four threads shuffle
-    for (long long u0 = (long long)blockIdx.x * blockDim.x; u0 < units; u0 += step) {
-        const long long u = u0 + threadIdx.x;
-        const long long px = u / per;
-        const int r = (int)(u - px * per), c0 = r * 8;
+    const long long units = p.pixels * per;
+    const long long u0 = (long long)blockIdx.x * (kQThreads * kQUnits) + threadIdx.x;
+    Raw8<T, V> raw[kQUnits];
+    QPlace at[kQUnits];
+#pragma unroll
+    for (int k = 0; k < kQUnits; ++k) {
+        const long long u = u0 + k * kQThreads;
+        at[k].px = kFlat ? 0 : u / per;
+        at[k].r = kFlat ? 0 : (int)(u - at[k].px * per);
+        const T* row = kFlat ? src + u * 8 : src + at[k].px * p.C;
         const bool in = u < units;
-        const T* row = src + px * p.C;
-        Raw8<T, V> raw;
-        float x[8];
-        if (in && in_bounds(&g_block_status, row, (long long)p.C * sizeof(T), p.src, x_bytes))
-            load8<T, V>(raw, row, c0, 1, p.C);
+        if (in && in_bounds(&g_block_status, row, (kFlat ? 8 : p.C) * (long long)sizeof(T), p.src, x_bytes))
+            load8<T, V>(raw[k], row, at[k].r * 8, 1, kFlat ? 8 : p.C);
         else
-            zero8<T, V>(raw);
-        unpack8<T, V>(raw, x);
+            zero8<T, V>(raw[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kQUnits; ++k) {
+        const long long u = u0 + k * kQThreads;
+        float x[8];
+        unpack8<T, V>(raw[k], x);
         // magnitudes as integers, whose order is the floats' and puts NaN on top
         uint32_t a = 0u;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) a = max(a, __float_as_uint(x[k]) & 0x7fffffffu);
+        for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(x[j]) & 0x7fffffffu);
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
         const int c = a == 0u ? 1 : scale_byte(__uint_as_float(a), fmt);
-        if (!in) continue;
-        if ((r & 3) == 0 &&
-            in_bounds(&g_block_status, scales + px * p.groups + (r >> 2), 1, p.scales, s_bytes))
-            scales[px * p.groups + (r >> 2)] = (uint8_t)c;
+        if (u >= units) continue;  // (whole groups of four threads)
+        const int c0 = at[k].r * 8;
+        uint8_t* sc = kFlat ? scales + (u >> 2) : scales + at[k].px * p.groups + (at[k].r >> 2);
+        if ((threadIdx.x & 3) == 0 && in_bounds(&g_block_status, sc, 1, p.scales, s_bytes))
+            *sc = (uint8_t)c;
         const uint2 w = encode8(x, c, fmt);
-        uint8_t* out = codes + px * p.code_bytes;
-        if constexpr (V) {
-            if (c0 < p.C) {
-                if (fmt == kQE2m1) *reinterpret_cast<uint32_t*>(out + c0 / 2) = w.x;
-                else *reinterpret_cast<uint2*>(out + c0) = w;
-            }
-        } else if (fmt == kQE2m1) {
-            for (int k = 0; k < 4; ++k)
-                if (c0 / 2 + k < p.code_bytes) out[c0 / 2 + k] = (uint8_t)(w.x >> (8 * k));
+        if constexpr (kFlat) {
+            if (fmt == kQE2m1) *reinterpret_cast<uint32_t*>(codes + u * 4) = w.x;
+            else *reinterpret_cast<uint2*>(codes + u * 8) = w;
         } else {
-            for (int k = 0; k < 8; ++k)
-                if (c0 + k < p.C) out[c0 + k] = (uint8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
+            uint8_t* out = codes + at[k].px * p.code_bytes;
+            if constexpr (V) {
+                if (c0 < p.C) {
+                    if (fmt == kQE2m1) *reinterpret_cast<uint32_t*>(out + c0 / 2) = w.x;
+                    else *reinterpret_cast<uint2*>(out + c0) = w;
+                }
+            } else if (fmt == kQE2m1) {
+                for (int j = 0; j < 4; ++j)
+                    if (c0 / 2 + j < p.code_bytes) out[c0 / 2 + j] = (uint8_t)(w.x >> (8 * j));
+            } else {
+                for (int j = 0; j < 8; ++j)
+                    if (c0 + j < p.C) out[c0 + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+            }
         }
     }
 }
 
-template <typename T, bool V>
-__global__ void __launch_bounds__(256) qcache_read_kernel(const __grid_constant__ QCacheJob p,
-                                                          int fmt) {
+template <typename T, bool V, bool kFlat>
+__global__ void __launch_bounds__(kQThreads) qcache_read_kernel(const __grid_constant__ QCacheJob p,
+                                                                int fmt) {
     const int n = blockIdx.y / p.frames, i = blockIdx.y - n * p.frames;
     const long long slot = (long long)n * p.slots + (p.slot + i) % p.slots;
     T* dst = static_cast<T*>(p.dst) + (long long)blockIdx.y * p.pixels * p.C;
@@ -176,29 +201,47 @@ __global__ void __launch_bounds__(256) qcache_read_kernel(const __grid_constant_
     const long long o_bytes = (long long)p.N * p.frames * p.pixels * p.C * (long long)sizeof(T);
     const long long s_bytes = (long long)p.N * p.slots * p.pixels * p.groups;
     const int per = (p.C + 7) / 8;  // threads a pixel
-    const long long units = p.pixels * per, step = (long long)gridDim.x * blockDim.x;
-    for (long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x; u < units; u += step) {
-        const long long px = u / per;
-        const int r = (int)(u - px * per), c0 = r * 8;
-        const uint8_t* in = codes + px * p.code_bytes;
-        const uint8_t* sc = scales + px * p.groups + (r >> 2);
-        if (!in_bounds(&g_block_status, sc, 1, p.scales, s_bytes)) continue;
-        uint2 w = make_uint2(0u, 0u);
-        if constexpr (V) {
-            if (fmt == kQE2m1) w.x = *reinterpret_cast<const uint32_t*>(in + c0 / 2);
-            else w = *reinterpret_cast<const uint2*>(in + c0);
+    const long long units = p.pixels * per;
+    const long long u0 = (long long)blockIdx.x * (kQThreads * kQUnits) + threadIdx.x;
+    QPlace at[kQUnits];
+    uint2 w[kQUnits];
+    int c[kQUnits];
+    bool ok[kQUnits];
+#pragma unroll
+    for (int k = 0; k < kQUnits; ++k) {
+        const long long u = u0 + k * kQThreads;
+        at[k].px = kFlat ? 0 : u / per;
+        at[k].r = kFlat ? 0 : (int)(u - at[k].px * per);
+        const int c0 = at[k].r * 8;
+        const uint8_t* in = codes + at[k].px * p.code_bytes;
+        const uint8_t* sc = kFlat ? scales + (u >> 2) : scales + at[k].px * p.groups + (at[k].r >> 2);
+        w[k] = make_uint2(0u, 0u);
+        c[k] = 1;
+        ok[k] = u < units && in_bounds(&g_block_status, sc, 1, p.scales, s_bytes);
+        if (!ok[k]) continue;
+        c[k] = *sc;
+        if constexpr (kFlat) {
+            if (fmt == kQE2m1) w[k].x = *reinterpret_cast<const uint32_t*>(codes + u * 4);
+            else w[k] = *reinterpret_cast<const uint2*>(codes + u * 8);
+        } else if constexpr (V) {
+            if (fmt == kQE2m1) w[k].x = *reinterpret_cast<const uint32_t*>(in + c0 / 2);
+            else w[k] = *reinterpret_cast<const uint2*>(in + c0);
         } else if (fmt == kQE2m1) {
-            for (int k = 0; k < 4; ++k)
-                if (c0 / 2 + k < p.code_bytes) w.x |= (uint32_t)in[c0 / 2 + k] << (8 * k);
+            for (int j = 0; j < 4; ++j)
+                if (c0 / 2 + j < p.code_bytes) w[k].x |= (uint32_t)in[c0 / 2 + j] << (8 * j);
         } else {
-            for (int k = 0; k < 8; ++k)
-                if (c0 + k < p.C) (k < 4 ? w.x : w.y) |= (uint32_t)in[c0 + k] << (8 * (k & 3));
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j < p.C) (j < 4 ? w[k].x : w[k].y) |= (uint32_t)in[c0 + j] << (8 * (j & 3));
         }
+    }
+#pragma unroll
+    for (int k = 0; k < kQUnits; ++k) {
+        if (!ok[k]) continue;
         float x[8];
-        decode8(w, *sc, fmt, x);
-        T* row = dst + px * p.C;
-        if (in_bounds(&g_block_status, row, (long long)p.C * sizeof(T), p.dst, o_bytes))
-            store8<T, V>(pack8<T, V>(x), row, c0, 1, p.C);
+        decode8(w[k], c[k], fmt, x);
+        T* row = kFlat ? dst + (u0 + k * kQThreads) * 8 : dst + at[k].px * p.C;
+        if (in_bounds(&g_block_status, row, (kFlat ? 8 : p.C) * (long long)sizeof(T), p.dst, o_bytes))
+            store8<T, V>(pack8<T, V>(x), row, at[k].r * 8, 1, kFlat ? 8 : p.C);
     }
 }
 
