@@ -269,7 +269,7 @@ SimtShape simt_shape(long long M, long long N, long long K) {
         const int want = (int)std::max<long long>(1, std::min<long long>({2 * kSms / tiles, up(K, 128), 512}));
         const long long per = up(up(K, want), kPwK) * kPwK;
         const int splits = (int)std::max<long long>(1, up(K, per));
-        const int resident = t == 128 ? 1 : 4;  // blocks an SM, in equal shares of its time
+        const int resident = t == 128 ? 2 : 4;  // blocks an SM, in equal shares of its time
         const double c = std::ceil((double)tiles * splits / (kSms * resident)) * resident *
                          (double)t * t * (per + 32) * (t == 128 ? 1.0 : 1.4);
         if (c < cost) {
@@ -281,7 +281,7 @@ SimtShape simt_shape(long long M, long long N, long long K) {
 }
 size_t simt_ws(long long M, long long N, long long K) {
     const int s = simt_shape(M, N, K).splits;
-    return s > 1 ? pad256((size_t)s * M * N * 4) : 0;
+    return s > 1 ? pad256((size_t)s * M * up(N, 4) * 4 * 4) : 0;
 }
 
 // Column sums of dP: chunks of rows, one row of partials each.
@@ -346,8 +346,9 @@ TcShape tc_shape(long long M, int N, long long K, bool b_mn, bool res, bool pre)
     const bool parts = s.splits > 1;
     // staging: two buffers in turn a warp, for out and for pre; with pre and a
     // residual 32-column chunks, so that four operand stages are left
-    s.chunk = s.BN % 64 != 0 || (res && pre) ? 32 : 64;
-    s.n_bufs = parts ? 0 : 2;
+    // (partials: 32 fp32 columns, as many bytes as 64 of bf16)
+    s.chunk = !parts && (s.BN % 64 != 0 || (res && pre)) ? 32 : 64;
+    s.n_bufs = 2;
     s.n_pres = parts || !pre ? 0 : 2;
     s.res_bufs = parts || !res || N % 8 != 0 ? 0 : kPtResBufs;
     s.stages = 10;
@@ -400,6 +401,17 @@ bool encode2d(CUtensorMap* m, const void* base, long long rows, int cols, int ld
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map of fp32 partials [splits][M][ldp] in boxes of 32 x 32 of one split.
+bool encode_partials(CUtensorMap* m, float* base, int splits, long long M, int ldp) {
+    const cuuint64_t dims[3] = {(cuuint64_t)ldp, (cuuint64_t)M, (cuuint64_t)splits};
+    const cuuint64_t strides[2] = {(cuuint64_t)ldp * 4, (cuuint64_t)M * ldp * 4};
+    const cuuint32_t box[3] = {32, 32, 1}, es[3] = {1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, es,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 void set_tc_attrs() {
     constexpr int kDevices = 64;
     static std::atomic<bool> done[kDevices];
@@ -444,7 +456,8 @@ ccv3d_status run_tc(const void* A, int lda, const void* B, int ldb, long long M,
                      : encode2d(&p.tm_b, B, N, (int)K, ldb, 64, s.BN / 2));
     const int ch = s.chunk;
     if (s.splits > 1) {
-        p.partial = partial;
+        p.partial = true;
+        ok = ok && encode_partials(&p.tm_out, partial, s.splits, M, s.ldp);
     } else {
         p.bias = static_cast<const bf16*>(o.bias);
         p.residual = static_cast<const bf16*>(o.residual);
@@ -461,7 +474,6 @@ ccv3d_status run_tc(const void* A, int lda, const void* B, int ldb, long long M,
     if (!ok) return CCV3D_ERR_CUDA;
     p.M = M;
     p.N = N;
-    p.ldp = s.ldp;
     p.tiles_m = s.tiles_m;
     p.tiles_n = s.tiles_n;
     p.BN = s.BN;
@@ -485,10 +497,19 @@ ccv3d_status run_tc(const void* A, int lda, const void* B, int ldb, long long M,
     p.step_s = pairs / s.tiles_n / s.tiles_m;
     pw_tc_kernel<A_MN, B_MN><<<grid, kPtThreads, s.smem, st>>>(p);
     if (s.splits > 1) {
-        const long long blocks = std::min<long long>(up(M * N, 256), kSms * 16LL);
+        const long long blocks = std::min<long long>(up(M * (s.ldp / 4), 256), kSms * 16LL);
         pw_join_kernel<bf16><<<(unsigned)blocks, 256, 0, st>>>(partial, s.splits, s.ldp, o);
     }
     return launched();
+}
+
+// Rows up to which the warp-level kernel takes a bf16 product whose Cin is a
+// multiple of 8 (4096 x 4096: 8 rows 10.7, 16 rows 12.0, 32 rows 23 us, against
+// 15 to 18 us on the tensor-core kernel with its reduction split).
+constexpr int kMmaRows = 16;
+bool few_rows(const ccv3d_pointwise_desc* d) {
+    return d->pixels <= kPwFewRows ||
+           (d->dtype == CCV3D_BF16 && d->Cin % 8 == 0 && d->pixels <= kMmaRows);
 }
 
 // Workspaces, in the order of their parts.  Forward: packed x and w, partials.
@@ -498,7 +519,7 @@ struct FwdWs {
 FwdWs forward_ws(const ccv3d_pointwise_desc* d) {
     FwdWs w = {};
     const long long M = d->pixels;
-    if (M <= kPwFewRows) return w;
+    if (few_rows(d)) return w;
     if (d->dtype == CCV3D_FP32) {
         w.parts = simt_ws(M, d->Cout, d->Cin);
     } else {
@@ -555,6 +576,7 @@ ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb
     const SimtShape s = simt_shape(M, N, K);
     p.splits = s.splits;
     p.k_per_split = s.k_per_split;
+    p.ldp = (int)up(N, 4) * 4;
     p.o = o;
     p.o.partial = p.splits > 1 ? partial : nullptr;
     if (s.tiles > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;
@@ -562,27 +584,36 @@ ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb
     if (s.tile == 128) pw_simt_kernel<float, AK, BK, 128><<<grid, 256, 0, st>>>(p);
     else pw_simt_kernel<float, AK, BK, 64><<<grid, 256, 0, st>>>(p);
     if (p.splits > 1) {
-        const long long blocks = std::min<long long>(up(M * N, 256), kSms * 16LL);
-        pw_join_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(partial, p.splits, N, o);
+        const long long blocks = std::min<long long>(up(M * (p.ldp / 4), 256), kSms * 16LL);
+        pw_join_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(partial, p.splits, p.ldp, o);
     }
     return launched();
 }
 
 template <typename T, int MR, int CPW>
 void run_rows(const T* x, const T* w, int K, const PwOut& o, cudaStream_t st) {
-    const unsigned grid = (unsigned)up(o.N, 4 * CPW);
-    if (K % 8 == 0) pw_rows_kernel<T, MR, CPW, true><<<grid, 128, 0, st>>>(x, w, K, o);
-    else pw_rows_kernel<T, MR, CPW, false><<<grid, 128, 0, st>>>(x, w, K, o);
+    const unsigned grid = (unsigned)up(o.N, CPW);
+    if (K % 8 == 0) pw_rows_kernel<T, MR, CPW, true><<<grid, 256, 0, st>>>(x, w, K, o);
+    else pw_rows_kernel<T, MR, CPW, false><<<grid, 256, 0, st>>>(x, w, K, o);
 }
 
 template <typename T>
 ccv3d_status forward_type(const ccv3d_pointwise_desc* d, const void* x, const void* w,
                           const PwOut& o, void* ws, cudaStream_t st) {
-    if (d->pixels <= kPwFewRows) {
+    const long long M = d->pixels;
+    if (few_rows(d)) {
         const T *xt = static_cast<const T*>(x), *wt = static_cast<const T*>(w);
-        if (d->pixels == 1) run_rows<T, 1, 1>(xt, wt, d->Cin, o, st);
-        else if (d->pixels <= 4) run_rows<T, 4, 4>(xt, wt, d->Cin, o, st);
-        else run_rows<T, 8, 4>(xt, wt, d->Cin, o, st);
+        if constexpr (sizeof(T) == 2) {
+            if (d->Cin % 8 == 0) {
+                const unsigned grid = (unsigned)up(o.N, 8);
+                if (M <= 8) pw_rows_mma_kernel<1><<<grid, 256, 0, st>>>(xt, wt, d->Cin, o);
+                else pw_rows_mma_kernel<2><<<grid, 256, 0, st>>>(xt, wt, d->Cin, o);
+                return launched();
+            }
+        }
+        if (M == 1) run_rows<T, 1, 1>(xt, wt, d->Cin, o, st);
+        else if (M <= 4) run_rows<T, 4, 2>(xt, wt, d->Cin, o, st);
+        else run_rows<T, 8, 2>(xt, wt, d->Cin, o, st);
         return launched();
     }
     if constexpr (sizeof(T) == 4) {

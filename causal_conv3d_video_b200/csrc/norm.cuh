@@ -36,8 +36,8 @@
 //     in flight while this one is worked on.
 #pragma once
 #include "elem.cuh"
+#include "bulk.cuh"
 #include "params.h"
-#include "ptx.cuh"
 
 namespace ccv3d {
 
@@ -463,13 +463,6 @@ struct TileShape {
     int cap;         // bytes of a tile and tensor in shared memory
     int stages, vec_len;  // vec_len: channels the block's threads cover, the vectors' length
 };
-
-__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes,
-                                         uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar) : "memory");
-}
 
 struct TileSpan {
     long long from;  // byte of the tensor the copy starts at (a multiple of 16)

@@ -5,7 +5,9 @@
 // operands read in place: forward A = x, B = w (both contiguous along k), dx
 // A = dP (along k), B = w (along n), dw A = dP, B = x (both along m and n).
 #pragma once
+#include "bulk.cuh"
 #include "elem.cuh"
+#include "params.h"
 
 namespace ccv3d {
 
@@ -13,7 +15,7 @@ namespace ccv3d {
 struct PwOut {
     const void *bias, *residual;
     void *out, *pre;
-    float* partial;   // not NULL: D goes to partial[split][M][N] and nothing else
+    float* partial;   // not NULL: D goes to partial[split][M][ldp] and nothing else
     long long M;
     int N, act;
 };
@@ -22,7 +24,7 @@ struct PwSimt {
     const void *A, *B;
     long long sam, sak, sbn, sbk;  // element strides; one of each pair is 1
     long long M, K;
-    int N, splits, vec;  // vec: rows of both operands are 16-byte multiples
+    int N, ldp, splits, vec;  // vec: rows of both operands are 16-byte multiples
     long long k_per_split;
     PwOut o;
 };
@@ -42,32 +44,44 @@ __device__ __forceinline__ void pw_store(const PwOut& o, long long m, int n, flo
 
 constexpr int kPwK = 16, kPwPad = 4;
 
-// kV operand values of a thread: along k (row r, k0 .. k0 + kV - 1) or along the
-// row index (k, r0 .. ).  R: rows of the tile (256 threads fetch R x 16).
+// A thread's part of an operand tile of R rows x 16 k: kV values along k (k-major
+// operand) or along the rows, at `p`, which moves on by 16 k a step.
 template <typename T, bool KMAJOR, int R>
-__device__ __forceinline__ void pw_fetch(float (&v)[R / 16], const T* base, long long s_row,
-                                         long long s_k, long long row0, long long rows,
-                                         long long k0, long long k1, int tid, bool vec) {
-    constexpr int kV = R / 16, kPer = 16 / kV;  // threads along a row's 16 k
-    const long long r = KMAJOR ? row0 + tid / kPer : row0 + (tid & 15) * kV;
-    const long long k = KMAJOR ? k0 + tid % kPer * kV : k0 + (tid >> 4);
-    // (s_row = 1 or s_k = 1 along the contiguous direction)
-    const T* p = base + (KMAJOR ? r * s_row + k : k * s_k + r);
-    const bool whole = KMAJOR ? r < rows && k + kV <= k1 : k < k1 && r + kV <= rows;
-    if (whole && vec) {
-#pragma unroll
-        for (int i = 0; i < kV; i += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(p + i);
-            v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const bool in = KMAJOR ? r < rows && k + i < k1 : k < k1 && r + i < rows;
-            v[i] = in ? (float)p[i] : 0.0f;
-        }
+struct PwFetch {
+    static constexpr int kV = R / 16, kPer = 16 / kV;  // kPer threads along a row's 16 k
+    const T* p;
+    long long step;
+    int rows, k;  // rows there are from the thread's on (k-major: 0 or 1); its k in a step
+    bool vec;
+    __device__ __forceinline__ PwFetch(const T* base, long long s_row, long long s_k,
+                                       long long row0, long long n_rows, long long k0, int tid,
+                                       bool v) {
+        const long long r = KMAJOR ? row0 + tid / kPer : row0 + (tid & 15) * kV;
+        k = KMAJOR ? tid % kPer * kV : tid >> 4;
+        // (s_row = 1 or s_k = 1 along the contiguous direction)
+        p = base + (KMAJOR ? r * s_row + (k0 + k) : (k0 + k) * s_k + r);
+        step = KMAJOR ? kPwK : kPwK * s_k;
+        const long long left = n_rows - r;
+        rows = (int)(left <= 0 ? 0 : (left < kV ? left : kV));
+        vec = v && (KMAJOR || rows == kV);
     }
-}
+    // The values of the next step, of which `left` k remain from its first on.
+    __device__ __forceinline__ void operator()(float (&v)[kV], int left) {
+        const bool in = KMAJOR ? rows > 0 : left > k;
+        if (in && vec && (!KMAJOR || left >= k + kV)) {
+#pragma unroll
+            for (int i = 0; i < kV; i += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(p + i);
+                v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                v[i] = in && (KMAJOR ? k + i < left : i < rows) ? (float)p[i] : 0.0f;
+        }
+        p += step;
+    }
+};
 
 template <bool KMAJOR, int R>
 __device__ __forceinline__ void pw_put(float (*s)[R + kPwPad], const float (&v)[R / 16], int tid) {
@@ -88,9 +102,14 @@ __device__ __forceinline__ void pw_put(float (*s)[R + kPwPad], const float (&v)[
 // registers.  128 has the better ratio of FMAs to shared-memory reads; 64 is
 // for products whose edges or few tiles would idle much of it.
 template <typename T, bool AK, bool BK, int S>
-__global__ void __launch_bounds__(256) pw_simt_kernel(const __grid_constant__ PwSimt p) {
+__global__ void __launch_bounds__(256, S == 128 ? 2 : 4) pw_simt_kernel(
+    const __grid_constant__ PwSimt p) {
     constexpr int kT = S / 16, kH = kT / 4;
-    __shared__ float sa[2][kPwK][S + kPwPad], sb[2][kPwK][S + kPwPad];
+    typedef float Slab[2][kPwK][S + kPwPad];
+    __shared__ __align__(16) float smem[2 * 2 * kPwK * (S + kPwPad)];
+    Slab& sa = *reinterpret_cast<Slab*>(smem);
+    Slab& sb = *reinterpret_cast<Slab*>(smem + 2 * kPwK * (S + kPwPad));
+    static_assert(64 * S <= 2 * 2 * kPwK * (S + kPwPad), "half a tile fits the operands' buffers");
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int tiles_n = (p.N + S - 1) / S;
     const long long tile = blockIdx.x;
@@ -99,112 +118,154 @@ __global__ void __launch_bounds__(256) pw_simt_kernel(const __grid_constant__ Pw
     const long long kb = (long long)blockIdx.z * p.k_per_split;
     const long long ke = kb + p.k_per_split < p.K ? kb + p.k_per_split : p.K;
     const T *A = static_cast<const T*>(p.A), *B = static_cast<const T*>(p.B);
-    float acc[kT][kT] = {}, va[kT], vb[kT];
-    pw_fetch<T, AK, S>(va, A, p.sam, p.sak, m0, p.M, kb, ke, tid, p.vec);
-    pw_fetch<T, BK, S>(vb, B, p.sbn, p.sbk, n0, p.N, kb, ke, tid, p.vec);
+    // accumulators and b values as pairs: one instruction, two FMAs
+    f2 acc[kT][kT / 2];
+#pragma unroll
+    for (int i = 0; i < kT; ++i)
+#pragma unroll
+        for (int j = 0; j < kT / 2; ++j) acc[i][j] = f2_all(0.0f);
+    float va[kT], vb[kT];
+    PwFetch<T, AK, S> fa(A, p.sam, p.sak, m0, p.M, kb, tid, p.vec);
+    PwFetch<T, BK, S> fb(B, p.sbn, p.sbk, n0, p.N, kb, tid, p.vec);
+    int left = (int)(ke - kb);
+    fa(va, left);
+    fb(vb, left);
     int cur = 0;
-    for (long long k = kb; k < ke; k += kPwK, cur ^= 1) {
+    for (; left > 0; left -= kPwK, cur ^= 1) {
         pw_put<AK, S>(sa[cur], va, tid);
         pw_put<BK, S>(sb[cur], vb, tid);
         __syncthreads();
-        if (k + kPwK < ke) {
-            pw_fetch<T, AK, S>(va, A, p.sam, p.sak, m0, p.M, k + kPwK, ke, tid, p.vec);
-            pw_fetch<T, BK, S>(vb, B, p.sbn, p.sbk, n0, p.N, k + kPwK, ke, tid, p.vec);
+        if (left > kPwK) {
+            fa(va, left - kPwK);
+            fb(vb, left - kPwK);
         }
 #pragma unroll
         for (int kk = 0; kk < kPwK; ++kk) {
-            float a[kT], b[kT];
+            float a[kT];
+            f2 b[kT / 2];
 #pragma unroll
             for (int h = 0; h < kH; ++h) {
                 const float4 x = *reinterpret_cast<const float4*>(&sa[cur][kk][h * 64 + ty * 4]);
-                const float4 y = *reinterpret_cast<const float4*>(&sb[cur][kk][h * 64 + tx * 4]);
+                const ulonglong2 y =
+                    *reinterpret_cast<const ulonglong2*>(&sb[cur][kk][h * 64 + tx * 4]);
                 a[h * 4] = x.x; a[h * 4 + 1] = x.y; a[h * 4 + 2] = x.z; a[h * 4 + 3] = x.w;
-                b[h * 4] = y.x; b[h * 4 + 1] = y.y; b[h * 4 + 2] = y.z; b[h * 4 + 3] = y.w;
+                b[h * 2] = y.x;
+                b[h * 2 + 1] = y.y;
             }
 #pragma unroll
-            for (int i = 0; i < kT; ++i)
+            for (int i = 0; i < kT; ++i) {
+                const f2 a2 = f2_all(a[i]);
 #pragma unroll
-                for (int j = 0; j < kT; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < kT / 2; ++j) acc[i][j] = f2_fma(a2, b[j], acc[i][j]);
+            }
         }
         // (one barrier a step: the next step writes the other buffer, whose
         // readers passed this step's barrier)
     }
-    // Epilogue: everything is read before the first store (out may be the
-    // residual, so the compiler keeps a load after a store where it stands:
-    // one by one, 64 residual loads waited out 64 memory latencies).
+    // Epilogue, 64 rows of the tile at a time through shared memory: the loop over
+    // its values is then short (unrolled over the accumulators it outgrew the
+    // instruction cache) and runs along the rows of out.  Four values' residuals
+    // are read before their stores: out may be the residual, so the compiler
+    // keeps a load after a store where it stands.
     const PwOut& o = p.o;
-    auto row = [&](int i) { return m0 + (i >> 2) * 64 + ty * 4 + (i & 3); };
-    auto col = [&](int j) { return n0 + (j >> 2) * 64 + tx * 4 + (j & 3); };
-    if (o.partial != nullptr) {
-#pragma unroll
-        for (int i = 0; i < kT; ++i)
-#pragma unroll
-            for (int j = 0; j < kT; ++j)
-                if (row(i) < p.M && col(j) < p.N)
-                    o.partial[((long long)blockIdx.z * p.M + row(i)) * p.N + col(j)] = acc[i][j];
-        return;
-    }
     const T *bias = static_cast<const T*>(o.bias), *residual = static_cast<const T*>(o.residual);
-    float res[kT][kT];
-    if (residual != nullptr)
-#pragma unroll
-        for (int i = 0; i < kT; ++i)
-#pragma unroll
-            for (int j = 0; j < kT; ++j)
-                res[i][j] = row(i) < p.M && col(j) < p.N ? (float)residual[row(i) * o.N + col(j)] : 0.0f;
-    if (bias != nullptr)
-#pragma unroll
-        for (int j = 0; j < kT; ++j) {
-            const float b = col(j) < p.N ? (float)bias[col(j)] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < kT; ++i) acc[i][j] += b;
-        }
     const long long bytes = o.M * o.N * (long long)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < kT; ++i)
+    for (int h = 0; h < kH; ++h) {
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kT; ++j) {
-            if (row(i) >= p.M || col(j) >= p.N) continue;
-            T* out = static_cast<T*>(o.out) + row(i) * o.N + col(j);
-            if (!in_bounds(&g_block_status, out, sizeof(T), o.out, bytes)) continue;
-            if (o.pre != nullptr) static_cast<T*>(o.pre)[row(i) * o.N + col(j)] = (T)acc[i][j];
-            float u = act_of<T>(acc[i][j], o.act);
-            if (residual != nullptr) u += res[i][j];
-            *out = (T)u;
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int g = 0; g < kH; ++g)
+                *reinterpret_cast<ulonglong2*>(&smem[(ty * 4 + i) * S + g * 64 + tx * 4]) =
+                    make_ulonglong2(acc[h * 4 + i][g * 2], acc[h * 4 + i][g * 2 + 1]);
+        __syncthreads();
+        const long long mh = m0 + h * 64;
+        const int n = n0 + tid % S;  // (256 is a multiple of S: a thread's column)
+        if (n >= p.N) continue;
+        constexpr int kStep = 256 / S;  // rows a pass
+        if (o.partial != nullptr) {
+            float* dst = o.partial + ((long long)blockIdx.z * p.M + mh) * p.ldp + n;
+#pragma unroll 4
+            for (int r = tid / S; r < 64; r += kStep)
+                if (mh + r < p.M) dst[(long long)r * p.ldp] = smem[r * S + tid % S];
+            continue;
         }
+        const float b = bias != nullptr ? (float)bias[n] : 0.0f;
+#pragma unroll 1
+        for (int r = tid / S; r < 64; r += 4 * kStep) {
+            float res[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const long long m = mh + r + j * kStep;
+                res[j] = residual != nullptr && m < p.M ? (float)residual[m * o.N + n] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const long long m = mh + r + j * kStep;
+                T* out = static_cast<T*>(o.out) + m * o.N + n;
+                if (m >= p.M || !in_bounds(&g_block_status, out, sizeof(T), o.out, bytes)) continue;
+                const float u = smem[(r + j * kStep) * S + tid % S] + b;
+                if (o.pre != nullptr) static_cast<T*>(o.pre)[m * o.N + n] = (T)u;
+                *out = (T)(act_of<T>(u, o.act) + res[j]);
+            }
+        }
+    }
 }
 
-// The partials of a split reduction, added in order, through the epilogue.
+// The partials of a split reduction, added in order, through the epilogue; four
+// columns a thread (ldp, the partials' row, is a multiple of 4).
 template <typename T>
 __global__ void __launch_bounds__(256) pw_join_kernel(const float* partial, int splits, int ldp,
                                                       const __grid_constant__ PwOut o) {
-    const long long total = o.M * o.N, step = (long long)gridDim.x * blockDim.x;
+    const int per = ldp / 4;
+    const long long total = o.M * per, step = (long long)gridDim.x * blockDim.x;
+    const T *bias = static_cast<const T*>(o.bias), *residual = static_cast<const T*>(o.residual);
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-        const long long m = i / o.N;
-        const int n = (int)(i - m * o.N);
-        float u = 0.0f;
-        for (int s = 0; s < splits; ++s) u += partial[(s * o.M + m) * ldp + n];
-        pw_store<T>(o, m, n, u);
+        const long long m = i / per;
+        const int n = (int)(i - m * per) * 4;
+        float u[4] = {}, res[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool in = n + j < o.N;
+            res[j] = in && residual != nullptr ? (float)residual[m * o.N + n + j] : 0.0f;
+            b[j] = in && bias != nullptr ? (float)bias[n + j] : 0.0f;
+        }
+        const float* src = partial + m * ldp + n;
+#pragma unroll 4
+        for (int s = 0; s < splits; ++s) {
+            const float4 x = *reinterpret_cast<const float4*>(src + s * o.M * ldp);
+            u[0] += x.x; u[1] += x.y; u[2] += x.z; u[3] += x.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            T* out = static_cast<T*>(o.out) + m * o.N + n + j;
+            if (n + j >= o.N || !in_bounds(&g_block_status, out, sizeof(T), o.out,
+                                           o.M * o.N * (long long)sizeof(T)))
+                continue;
+            u[j] += b[j];
+            if (o.pre != nullptr) static_cast<T*>(o.pre)[m * o.N + n + j] = (T)u[j];
+            *out = (T)(act_of<T>(u[j], o.act) + res[j]);
+        }
     }
 }
 
-// Few rows (M <= kPwFewRows): bound by reading w once.  A warp takes CPW rows
-// of w (output channels) and all rows of x; its lanes split k, eight values a
-// load.  CPW = 1 for one row keeps the most warps loading; with several rows,
-// four output channels share each load of x.
+// Few rows on FFMA (fp32, and bf16 whose rows are no multiple of 8): bound by
+// reading w once.  A block of eight warps takes CPW rows of w (output channels)
+// and all MR rows of x; its lanes split k, eight values a load, the warps'
+// totals meet in shared memory.
 constexpr int kPwFewRows = 8;
 
 template <typename T, int MR, int CPW, bool V>
-__global__ void __launch_bounds__(128) pw_rows_kernel(const T* x, const T* w, int K,
+__global__ void __launch_bounds__(256) pw_rows_kernel(const T* x, const T* w, int K,
                                                       const __grid_constant__ PwOut o) {
-    const int lane = threadIdx.x & 31;
-    const int n0 = (int)((blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * CPW);
-    if (n0 >= o.N) return;
+    __shared__ float part[8][CPW * MR];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n0 = (int)blockIdx.x * CPW;
     float acc[CPW][MR] = {};
     const int M = (int)o.M;
-    const int kstep = 32 * 8;
-#pragma unroll 4
-    for (int k = 0; k < K; k += kstep) {
+#pragma unroll 2
+    for (int k = warp * 256; k < K; k += 8 * 256) {
         const int c0 = V ? k + lane * 8 : k + lane;
         Raw8<T, V> rw[CPW];
 #pragma unroll
@@ -212,20 +273,23 @@ __global__ void __launch_bounds__(128) pw_rows_kernel(const T* x, const T* w, in
             if (n0 + c < o.N) load8<T, V>(rw[c], w + (long long)(n0 + c) * K, c0, 32, K);
             else zero8<T, V>(rw[c]);
         }
-        float f[CPW][8];
+        f2 f[CPW][4];
 #pragma unroll
         for (int c = 0; c < CPW; ++c) unpack8<T, V>(rw[c], f[c]);
 #pragma unroll
         for (int m = 0; m < MR; ++m) {
             if (m >= M) break;
             Raw8<T, V> rx;
-            float g[8];
+            f2 g[4];
             load8<T, V>(rx, x + (long long)m * K, c0, 32, K);
             unpack8<T, V>(rx, g);
 #pragma unroll
-            for (int c = 0; c < CPW; ++c)
+            for (int c = 0; c < CPW; ++c) {
+                f2 t = f2_mul(f[c][0], g[0]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[c][m] = fmaf(f[c][i], g[i], acc[c][m]);
+                for (int i = 1; i < 4; ++i) t = f2_fma(f[c][i], g[i], t);
+                acc[c][m] += f2_sum(t);
+            }
         }
     }
 #pragma unroll
@@ -235,10 +299,126 @@ __global__ void __launch_bounds__(128) pw_rows_kernel(const T* x, const T* w, in
             float v = acc[c][m];
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-            // one lane per value
-            if (lane == ((c * MR + m) & 31) && m < M && n0 + c < o.N)
-                pw_store<T>(o, m, n0 + c, v);
+            if (lane == ((c * MR + m) & 31)) part[warp][c * MR + m] = v;
         }
+    __syncthreads();
+    for (int i = threadIdx.x; i < CPW * MR; i += 256) {
+        const int c = i / MR, m = i % MR;
+        if (m >= M || n0 + c >= o.N) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) v += part[s][i];
+        pw_store<T>(o, m, n0 + c, v);
+    }
+}
+
+// Few rows, bf16: still bound by reading w once, but FFMA would spend nine
+// instructions on each weight for eight rows (64 us for 8 x 4096 x 4096).  So
+// the warp-level matrix instruction (16 x 8 x 16), with the rows of x as its
+// 16-row operand and eight output channels as its columns, fed straight from
+// global memory: k may be taken in any order as long as both operands agree, so
+// a thread loads 16 bytes, eight consecutive k, of its rows of w and x and they
+// serve two instructions.  A block of eight warps takes 8 output channels (16
+// would leave SMs with one block beside SMs with two at 4096 channels); the
+// warps take turns along k and their totals meet in shared memory.  One thread
+// has w copied to shared memory in bulk, kRwStages chunks of 512 k ahead (24 KB a
+// block, seven blocks an SM, whatever the registers hold).  (tcgen05
+// tiles of 256 rows would be all but empty here, and their start-up alone is as
+// long as the whole read.)  MB: groups of 8 rows of x.
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+constexpr int kRwStages = 3, kRwK = 512;
+constexpr int kRwPitch = kRwK * 2 + 64;  // bytes of a row of a chunk: two rows' reads use all banks
+
+template <int MB>
+__global__ void __launch_bounds__(256) pw_rows_mma_kernel(const bf16_t* x, const bf16_t* w, int K,
+                                                          const __grid_constant__ PwOut o) {
+    constexpr int kTiles = (MB + 1) / 2;
+    __shared__ __align__(16) uint8_t ring[kRwStages][8][kRwPitch];
+    __shared__ float part[8][kTiles * 16][8 + 1];
+    __shared__ __align__(8) uint64_t full[kRwStages];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int n0 = (int)blockIdx.x * 8, M = (int)o.M;
+    const int chunks = (K + kRwK - 1) / kRwK;
+    auto issue = [&](int c) {
+        const int k0 = c * kRwK;
+        const uint32_t bytes = (uint32_t)min(kRwK, K - k0) * 2;  // (K is a multiple of 8)
+        const uint32_t bar = smem_u32(&full[c % kRwStages]);
+        mbar_arrive_expect_tx(bar, 8 * bytes);
+        for (int r = 0; r < 8; ++r) {
+            // channels past the end read as the last one (and are not stored)
+            const bf16_t* from = w + (long long)min(n0 + r, o.N - 1) * K + k0;
+            bulk_g2s(smem_u32(ring[c % kRwStages][r]), from, bytes, bar);
+        }
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRwStages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        fence_mbar_init();
+        for (int c = 0; c < kRwStages && c < chunks; ++c) issue(c);
+    }
+    __syncthreads();
+    float acc[kTiles][4] = {};
+    const bf16_t* xr[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) xr[m] = x + (long long)(m * 8 + g < M ? m * 8 + g : 0) * K;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    bool live = true;
+    for (int c = 0; c < chunks; ++c) {
+        // this thread's two 32-wide steps of the chunk; x is read before the wait
+        uint4 rx[2][kTiles * 2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int k = c * kRwK + (u * 8 + warp) * 32 + t * 8;
+#pragma unroll
+            for (int m = 0; m < kTiles * 2; ++m)
+                rx[u][m] = m < MB && k < K ? *reinterpret_cast<const uint4*>(xr[m < MB ? m : 0] + k)
+                                           : zero;
+        }
+        const int st = c % kRwStages;
+        if (live && !mbar_wait(smem_u32(&full[st]), (uint32_t)(c / kRwStages & 1), &g_block_status,
+                               kWaitLimitNs))
+            live = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int kk = (u * 8 + warp) * 32 + t * 8;
+            const uint4 rw = c * kRwK + kk < K
+                                 ? *reinterpret_cast<const uint4*>(ring[st][g] + kk * 2) : zero;
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m) {
+                mma_16816(acc[m], rx[u][2 * m].x, rx[u][2 * m + 1].x, rx[u][2 * m].y,
+                          rx[u][2 * m + 1].y, rw.x, rw.y);
+                mma_16816(acc[m], rx[u][2 * m].z, rx[u][2 * m + 1].z, rx[u][2 * m].w,
+                          rx[u][2 * m + 1].w, rw.z, rw.w);
+            }
+        }
+        if (c + kRwStages < chunks) {
+            __syncthreads();  // every warp is done with the chunk
+            if (threadIdx.x == 0) issue(c + kRwStages);
+        }
+    }
+    // d0, d1: row g, channels 2t and 2t + 1; d2, d3: row g + 8
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            part[warp][m * 16 + g + (i >> 1) * 8][2 * t + (i & 1)] = acc[m][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTiles * 128; i += 256) {
+        const int n = i & 7, m = i >> 3;  // channels side by side
+        if (m >= M || n0 + n >= o.N) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) v += part[s][m][n];
+        pw_store<bf16_t>(o, m, n0 + n, v);
+    }
 }
 
 // dP = dout act'(pre) into dp (rows of ldp elements, those past N zeros), and

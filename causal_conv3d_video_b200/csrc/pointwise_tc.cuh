@@ -46,13 +46,13 @@ constexpr int kPtA = 128 * kPtK * 2;     // bytes of A a CTA and stage
 constexpr int kPtBox = 64 * kPtK * 2;    // one mn-major box
 
 struct PtParams {
-    CUtensorMap tm_a, tm_b, tm_out, tm_res, tm_pre;
+    CUtensorMap tm_a, tm_b, tm_out, tm_res, tm_pre;  // tm_out: of the partials where there are
     const bf16_t* bias;
     const bf16_t* residual;  // direct: plain loads and stores instead of TMA
     bf16_t *out, *pre;
-    float* partial;          // not NULL: fp32 partials [split][M][ldp] only
+    bool partial;            // D goes to fp32 partials [split][M][ldp] and nothing else
     long long M;
-    int N, ldp, act, direct;
+    int N, act, direct;
     int tiles_m, tiles_n, BN, kblocks, splits, kb_per_split, stages, tmem_cols;
     int chunk;               // columns the epilogue moves at a time: 64 or 32
     int n_bufs, n_pres;      // staging buffers of an epilogue warp
@@ -75,6 +75,12 @@ __device__ __forceinline__ void pt_load(uint32_t dst, const CUtensorMap* m, uint
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4}], [%2];"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void pt_store_3d(const CUtensorMap* m, uint32_t src, int c0, int c1,
+                                            int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(m)), "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
 }
 __device__ __forceinline__ void pt_store(const CUtensorMap* m, uint32_t src, int c0, int c1) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
@@ -116,7 +122,7 @@ __host__ __device__ constexpr int pt_b_bytes(bool mn, int bn) {
     return mn ? ((bn / 2 + 63) / 64) * kPtBox : (bn / 2) * kPtK * 2;
 }
 __host__ __device__ constexpr size_t pt_smem(bool b_mn, int bn, int stages, int chunk,
-                                             int bufs, int res_bufs) {
+                                             int bufs, int res_bufs) {  // chunk: bytes / 2 of a row
     return 1024 + (size_t)stages * (kPtA + pt_b_bytes(b_mn, bn)) +
            (size_t)chunk * 2 * (kPtEpiWarps * 32 * bufs + 128 * res_bufs) +
            (size_t)bn * 4 * 2 + (size_t)(2 * stages + 2 * kPtAccs + 4 + 2 * kPtResBufs) * 8 + 16;
@@ -170,7 +176,7 @@ template <int kCh>
 __device__ __forceinline__ void pt_ahead(const PtParams& p, const PtShared& sh, int pair, int G,
                                          uint32_t rank, int lane) {
     constexpr uint32_t kBytes = 128 * kCh * 2;
-    if (p.partial != nullptr) return;
+    if (p.partial) return;
     const int nch = p.BN / kCh;
     Ring ring;
     int issued = 0;
@@ -209,17 +215,19 @@ __device__ __forceinline__ void pt_ahead(const PtParams& p, const PtShared& sh, 
 }
 
 // The epilogue of one warp: every second chunk of kCh columns of its 32 rows.
-template <int kCh>
+// kPart: chunks of 32 columns go out as fp32 partials.
+template <int kCh, bool kPart>
 __device__ __forceinline__ void pt_epilogue(const PtParams& p, const PtShared& sh, uint32_t tmem,
                                             int pair, int G, uint32_t rank, bool leader, int warp,
                                             int lane) {
-    constexpr int kRowB = kCh * 2, kBuf = 32 * kRowB;
+    constexpr int kRowB = kPart ? 128 : kCh * 2, kBuf = 32 * kRowB;
+    static_assert(!kPart || kCh == 32, "partials: 32 fp32 columns are a 128-byte row");
     const int q = warp & 3, wid = warp - 4, set = wid >> 2;
     const int nch = p.BN / kCh;
     uint8_t* bufs = sh.staging + (size_t)wid * kBuf * (p.n_bufs + p.n_pres);
     uint8_t* pres = bufs + (size_t)p.n_bufs * kBuf;
     const uint32_t empty_leader = pt_mapa(smem_u32(sh.acc_empty), 0);
-    const bool whole = p.partial == nullptr, biased = whole && p.bias != nullptr;
+    const bool biased = !kPart && p.bias != nullptr;
     int turn = 0;  // staging buffer
     int first = 0;  // chunks of the tiles before this one
     Ring acc;
@@ -268,24 +276,25 @@ __device__ __forceinline__ void pt_epilogue(const PtParams& p, const PtShared& s
                 }
             }
             if (c + 2 >= nch) drained();
-            if (!whole) {
-                const long long r = (long long)r0 + lane;
-                if (in && ok && r < p.M) {
-                    float* dst = p.partial + ((long long)w.split * p.M + r) * p.ldp + c0;
-#pragma unroll
-                    for (int i = 0; i < kCh; i += 4)
-                        if (c0 + i < p.ldp &&
-                            in_bounds(&g_block_status, dst + i, 16, p.partial,
-                                      (long long)p.splits * p.M * p.ldp * 4))
-                            *reinterpret_cast<uint4*>(dst + i) =
-                                make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                }
-                continue;
-            }
             // the store before the last one has been read: its buffer is free
             if (lane == 0) bulk_wait_group_read1();
             __syncwarp();
             uint8_t* buf = bufs + turn * kBuf;
+            if constexpr (kPart) {
+#pragma unroll
+                for (int i = 0; i < kCh / 4; ++i)
+                    *reinterpret_cast<uint4*>(buf + lane * kRowB +
+                                              (swizzled_chunk<kRowB>(i, lane) << 4)) =
+                        make_uint4(v[i * 4], v[i * 4 + 1], v[i * 4 + 2], v[i * 4 + 3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (in && ok) pt_store_3d(&p.tm_out, smem_u32(buf), c0, r0, w.split);
+                    bulk_commit_group();
+                }
+                turn ^= 1;
+                continue;
+            }
             uint8_t* pre = pres + turn * kBuf;
             if (p.pre != nullptr) {
 #pragma unroll
@@ -533,8 +542,12 @@ pw_tc_kernel(const __grid_constant__ PtParams p) {
         if (p.chunk == 64) pt_ahead<64>(p, sh, pair, G, rank, lane);
         else pt_ahead<32>(p, sh, pair, G, rank, lane);
     } else if (warp >= 4) {
-        if (p.chunk == 64) pt_epilogue<64>(p, sh, tmem_base, pair, G, rank, leader, warp, lane);
-        else pt_epilogue<32>(p, sh, tmem_base, pair, G, rank, leader, warp, lane);
+        if (p.partial)
+            pt_epilogue<32, true>(p, sh, tmem_base, pair, G, rank, leader, warp, lane);
+        else if (p.chunk == 64)
+            pt_epilogue<64, false>(p, sh, tmem_base, pair, G, rank, leader, warp, lane);
+        else
+            pt_epilogue<32, false>(p, sh, tmem_base, pair, G, rank, leader, warp, lane);
     }
     __syncwarp();
     tc_fence_before();

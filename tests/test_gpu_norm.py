@@ -75,10 +75,14 @@ def _check_forward(s, h0=None, got=None):
 SHAPES = [(1, 8), (1, 768), (3, 1), (5, 7), (33, 16), (17, 24), (64, 32), (129, 75), (100, 96),
           (31, 100), (77, 192), (50, 257), (40, 384), (9, 513), (23, 768), (21, 1000), (6, 1025),
           (5, 2048), (3, 4096), (2, 8185), (2, 8192)]
+# enough rows for the tiles of rows (forward), odd ones for their ragged ends
+TILED = [(5003, 1), (1009, 8), (777, 24), (2001, 32), (1500, 50), (3001, 75), (2300, 96), (701, 99),
+         (1234, 160), (999, 192), (640, 257), (1111, 384), (401, 500), (333, 720), (600, 767),
+         (500, 768), (700, 769), (350, 1000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("rows,C", SHAPES)
+@pytest.mark.parametrize("rows,C", SHAPES + TILED)
 def test_forward_shapes(rows, C, dtype):
     _check_forward(_case(rows, C, dtype, actk="silu"))
     _check_forward(_case(rows, C, dtype, residual=True, gates=1, post="rms", actk="silu", seed=1))
@@ -93,6 +97,17 @@ def test_forward_shapes(rows, C, dtype):
 def test_forward_forms(pre, post, gates, bias, weights):
     _check_forward(_case(60, 96, "bf16", pre=pre, post=post, residual=True, gates=gates, bias=bias,
                          weights=weights, actk="none"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gate_rows_in_tiles(dtype):
+    """Gate rows that change inside a tile, and groups of one row, three, many."""
+    for rows, C, gates in [(1200, 96, 1200), (1200, 96, 400), (1300, 75, 13), (900, 193, 3),
+                           (700, 768, 100), (1400, 40, 7)]:
+        s = _case(rows, C, dtype, residual=True, gates=gates, post="rms", actk="silu", seed=gates)
+        _check_forward(s)
+        _check_backward(s)
+        _check_forward(_case(rows, C, dtype, residual=True, gates=gates, post="layer", bias=True))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -237,7 +252,7 @@ def _check_backward(s, want=None, dh_out=True):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("rows,C", SHAPES)
+@pytest.mark.parametrize("rows,C", SHAPES + TILED)
 def test_backward_shapes(rows, C, dtype):
     _check_backward(_case(rows, C, dtype, actk="silu"))
     _check_backward(_case(rows, C, dtype, residual=True, gates=1, post="rms", actk="silu", seed=1))
