@@ -313,38 +313,69 @@ def ccv3d_selftest_bounds(stream=None) -> int:
 
 
 # ------------------------------------------- the operators around the convolution
-_TORCH_DTYPES = None
+# torch's types and the cheapest queries of the current device and stream,
+# looked up at the first call (a call of a few microseconds is bound by this
+# binding's own time)
+_dtypes = _device_now = _stream_now = None
 
 
-def _operands(where, dtype, pairs):
-    """Device addresses of a call's buffers.  pairs: (name, tensor or address
-    or None, elements or None, torch dtype name or None for the call's).
-    Tensors must be contiguous, of the element type and size the call reads or
-    writes, on the current CUDA device; raises ValueError otherwise.  Raw
-    addresses are the caller's word."""
+def _first_call():
+    global _dtypes, _device_now, _stream_now
     import torch
-    global _TORCH_DTYPES
-    if _TORCH_DTYPES is None:
-        _TORCH_DTYPES = {CCV3D_BF16: torch.bfloat16, CCV3D_FP32: torch.float32,
-                         "uint8": torch.uint8}
+    _device_now = torch.cuda.current_device
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _stream_now = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _dtypes = {CCV3D_BF16: torch.bfloat16, CCV3D_FP32: torch.float32, "uint8": torch.uint8}
+
+
+def _refuse(where, name, t, n, want, device):
+    if want is not None and t.dtype is not want:
+        raise ValueError(f"{where}: {name} is {t.dtype}, not {want}")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{where}: {name} has {t.numel()} elements, not {n}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} is not contiguous")
+    raise ValueError(f"{where}: {name} is on {t.device}, not on the current CUDA device {device}")
+
+
+def _operands(where, dtype, stream, tensors, extra=()):
+    """Device addresses of a call's buffers, then the stream's.  tensors: (name,
+    tensor or address or None, elements) of the call's element type; extra:
+    (name, tensor, elements, type) of others.  Tensors must be contiguous, of the
+    type and size the call reads or writes, on the current CUDA device; raises
+    ValueError otherwise.  Raw addresses are the caller's word."""
+    if _dtypes is None:
+        _first_call()
+    want = _dtypes.get(dtype)
     out, device = [], None
-    for name, t, n, dt in pairs:
-        if t is None or isinstance(t, int):
+    for name, t, n in tensors:
+        if t is None or type(t) is int:
             out.append(t)
             continue
-        want = _TORCH_DTYPES.get(dtype if dt is None else dt)
-        if want is not None and t.dtype != want:
-            raise ValueError(f"{where}: {name} is {t.dtype}, not {want}")
-        if n is not None and t.numel() != n:
-            raise ValueError(f"{where}: {name} has {t.numel()} elements, not {n}")
-        if not t.is_contiguous():
-            raise ValueError(f"{where}: {name} is not contiguous")
+        d = t.get_device()
         if device is None:
-            device = torch.cuda.current_device() if t.is_cuda else -1
-        if not t.is_cuda or t.get_device() != device:
-            raise ValueError(f"{where}: {name} is on {t.device}, not on the current CUDA device")
+            device = _device_now() if d >= 0 else -2
+        if (d != device or t.numel() != n or not t.is_contiguous()
+                or (t.dtype is not want and want is not None)):
+            _refuse(where, name, t, n, want, device)
         out.append(t.data_ptr())
-    return out
+    for name, t, n, dt in extra:
+        if t is None or type(t) is int:
+            out.append(t)
+            continue
+        d = t.get_device()
+        if device is None:
+            device = _device_now() if d >= 0 else -2
+        other = _dtypes.get(dt)
+        if (d != device or (n is not None and t.numel() != n) or not t.is_contiguous()
+                or (t.dtype is not other and other is not None)):
+            _refuse(where, name, t, n, other, device)
+        out.append(t.data_ptr())
+    if stream is None:
+        stream = _stream_now(_device_now() if device is None else device)
+    elif type(stream) is not int:
+        stream = stream.cuda_stream
+    return out, stream
 
 
 def _status(rc, where, check):
@@ -353,11 +384,9 @@ def _status(rc, where, check):
     return rc
 
 
-def _ws(where, ws):
-    """Address and bytes of a workspace: a tensor (any type, contiguous) or None."""
-    if ws is None:
-        return None, 0
-    return _operands(where, "any", [("ws", ws, None, "any")])[0], ws.numel() * ws.element_size()
+def _bytes(ws):
+    """Size of a workspace: a tensor of any type, or None."""
+    return 0 if ws is None else ws.numel() * ws.element_size()
 
 
 def ccv3d_norm_workspace(desc: ccv3d_norm_desc) -> int:
@@ -369,14 +398,14 @@ def ccv3d_norm_forward(desc: ccv3d_norm_desc, h, b, gate, post_w, post_bias, pre
     """h_out = h + scale * gate * post(b); y = act(pre(h_out)).  Tensors as the
     C call's comment lists them (None for NULL).  Raises CCV3DError on a
     refused call unless check=False."""
-    n, C = desc.rows * desc.C, desc.C
-    gates = n // desc.gate_rows if gate is not None and desc.gate_rows > 0 else None
-    a = _operands("ccv3d_norm_forward", desc.dtype, (
-        ("h", h, n, None), ("b", b, n, None), ("gate", gate, gates, None),
-        ("post_w", post_w, C, None), ("post_bias", post_bias, C, None), ("pre_w", pre_w, C, None),
-        ("pre_bias", pre_bias, C, None), ("h_out", h_out, n, None), ("y", y, n, None)))
-    return _status(lib.ccv3d_norm_forward(ctypes.byref(desc), *a, _stream(stream)),
-                   "ccv3d_norm_forward", check)
+    C = desc.C
+    n = desc.rows * C
+    gates = n // max(1, desc.gate_rows) if gate is not None else 0
+    a, st = _operands("ccv3d_norm_forward", desc.dtype, stream, (
+        ("h", h, n), ("b", b, n), ("gate", gate, gates), ("post_w", post_w, C),
+        ("post_bias", post_bias, C), ("pre_w", pre_w, C), ("pre_bias", pre_bias, C),
+        ("h_out", h_out, n), ("y", y, n)))
+    return _status(lib.ccv3d_norm_forward(desc, *a, st), "ccv3d_norm_forward", check)
 
 
 def ccv3d_norm_backward(desc: ccv3d_norm_desc, h_out, b, gate, post_w, post_bias, pre_w, pre_bias,
@@ -384,18 +413,17 @@ def ccv3d_norm_backward(desc: ccv3d_norm_desc, h_out, b, gate, post_w, post_bias
                         stream=None, check: bool = True) -> int:
     """Gradients of ccv3d_norm_forward (None for those not wanted); ws: a
     workspace of at least ccv3d_norm_workspace(desc) bytes."""
-    n, C = desc.rows * desc.C, desc.C
-    gates = n // desc.gate_rows if gate is not None and desc.gate_rows > 0 else None
+    C = desc.C
+    n = desc.rows * C
+    gates = n // max(1, desc.gate_rows) if gate is not None else 0
     where = "ccv3d_norm_backward"
-    a = _operands(where, desc.dtype, (
-        ("h_out", h_out, n, None), ("b", b, n, None), ("gate", gate, gates, None),
-        ("post_w", post_w, C, None), ("post_bias", post_bias, C, None), ("pre_w", pre_w, C, None),
-        ("pre_bias", pre_bias, C, None), ("dy", dy, n, None), ("dh_out", dh_out, n, None),
-        ("dh", dh, n, None), ("db", db, n, None), ("dgate", dgate, gates, None),
-        ("dpost_w", dpost_w, C, None), ("dpost_bias", dpost_bias, C, None),
-        ("dpre_w", dpre_w, C, None), ("dpre_bias", dpre_bias, C, None)))
-    return _status(lib.ccv3d_norm_backward(ctypes.byref(desc), *a, *_ws(where, ws),
-                                           _stream(stream)), where, check)
+    a, st = _operands(where, desc.dtype, stream, (
+        ("h_out", h_out, n), ("b", b, n), ("gate", gate, gates), ("post_w", post_w, C),
+        ("post_bias", post_bias, C), ("pre_w", pre_w, C), ("pre_bias", pre_bias, C),
+        ("dy", dy, n), ("dh_out", dh_out, n), ("dh", dh, n), ("db", db, n),
+        ("dgate", dgate, gates), ("dpost_w", dpost_w, C), ("dpost_bias", dpost_bias, C),
+        ("dpre_w", dpre_w, C), ("dpre_bias", dpre_bias, C)), (("ws", ws, None, None),))
+    return _status(lib.ccv3d_norm_backward(desc, *a, _bytes(ws), st), where, check)
 
 
 def ccv3d_pointwise_workspace(desc: ccv3d_pointwise_desc):
@@ -412,11 +440,10 @@ def ccv3d_pointwise_forward(desc: ccv3d_pointwise_desc, x, w, bias, residual, ou
     argument of act."""
     M, K, N = desc.pixels, desc.Cin, desc.Cout
     where = "ccv3d_pointwise_forward"
-    a = _operands(where, desc.dtype, (
-        ("x", x, M * K, None), ("w", w, N * K, None), ("bias", bias, N, None),
-        ("residual", residual, M * N, None), ("out", out, M * N, None), ("pre", pre, M * N, None)))
-    return _status(lib.ccv3d_pointwise_forward(ctypes.byref(desc), *a, *_ws(where, ws),
-                                               _stream(stream)), where, check)
+    a, st = _operands(where, desc.dtype, stream, (
+        ("x", x, M * K), ("w", w, N * K), ("bias", bias, N), ("residual", residual, M * N),
+        ("out", out, M * N), ("pre", pre, M * N)), (("ws", ws, None, None),))
+    return _status(lib.ccv3d_pointwise_forward(desc, *a, _bytes(ws), st), where, check)
 
 
 def ccv3d_pointwise_backward(desc: ccv3d_pointwise_desc, x, w, pre, dout, dx, dw, dbias, ws,
@@ -424,12 +451,10 @@ def ccv3d_pointwise_backward(desc: ccv3d_pointwise_desc, x, w, pre, dout, dx, dw
     """Gradients of ccv3d_pointwise_forward (None for those not wanted)."""
     M, K, N = desc.pixels, desc.Cin, desc.Cout
     where = "ccv3d_pointwise_backward"
-    a = _operands(where, desc.dtype, (
-        ("x", x, M * K, None), ("w", w, N * K, None), ("pre", pre, M * N, None),
-        ("dout", dout, M * N, None), ("dx", dx, M * K, None), ("dw", dw, N * K, None),
-        ("dbias", dbias, N, None)))
-    return _status(lib.ccv3d_pointwise_backward(ctypes.byref(desc), *a, *_ws(where, ws),
-                                                _stream(stream)), where, check)
+    a, st = _operands(where, desc.dtype, stream, (
+        ("x", x, M * K), ("w", w, N * K), ("pre", pre, M * N), ("dout", dout, M * N),
+        ("dx", dx, M * K), ("dw", dw, N * K), ("dbias", dbias, N)), (("ws", ws, None, None),))
+    return _status(lib.ccv3d_pointwise_backward(desc, *a, _bytes(ws), st), where, check)
 
 
 def ccv3d_qcache_sizes(desc: ccv3d_qcache_desc):
@@ -440,48 +465,46 @@ def ccv3d_qcache_sizes(desc: ccv3d_qcache_desc):
     return c.value, s.value
 
 
-def _ring_bytes(desc):
+def _ring(desc, codes, scales):
+    """The two buffers of a quantised ring, for _operands."""
     px = desc.N * desc.ring_slots * desc.H * desc.W
-    return (px * ((desc.C + 1) // 2 if desc.format == QFORMATS["e2m1"] else desc.C),
-            px * ((desc.C + 31) // 32))
+    C = desc.C
+    return (("codes", codes, px * ((C + 1) // 2 if desc.format == 2 else C), "uint8"),
+            ("scales", scales, px * ((C + 31) // 32), "uint8"))
 
 
 def ccv3d_qcache_write(desc: ccv3d_qcache_desc, x, T_x: int, first: int, frames: int, slot: int,
                        codes, scales, stream=None, check: bool = True) -> int:
     """Quantise frames [first, first + frames) of x into ring slots from `slot` on."""
-    cb, sb = _ring_bytes(desc)
-    a = _operands("ccv3d_qcache_write", desc.dtype, (
-        ("x", x, desc.N * T_x * desc.H * desc.W * desc.C, None), ("codes", codes, cb, "uint8"),
-        ("scales", scales, sb, "uint8")))
-    return _status(lib.ccv3d_qcache_write(ctypes.byref(desc), a[0], T_x, first, frames, slot, a[1],
-                                          a[2], _stream(stream)), "ccv3d_qcache_write", check)
+    n = desc.N * T_x * desc.H * desc.W * desc.C
+    a, st = _operands("ccv3d_qcache_write", desc.dtype, stream, (("x", x, n),),
+                      _ring(desc, codes, scales))
+    return _status(lib.ccv3d_qcache_write(desc, a[0], T_x, first, frames, slot, a[1], a[2], st),
+                   "ccv3d_qcache_write", check)
 
 
 def ccv3d_qcache_read(desc: ccv3d_qcache_desc, codes, scales, head: int, frames: int, out,
                       stream=None, check: bool = True) -> int:
     """Read ring slots from `head` on back into `frames` dense frames."""
-    cb, sb = _ring_bytes(desc)
-    a = _operands("ccv3d_qcache_read", desc.dtype, (
-        ("codes", codes, cb, "uint8"), ("scales", scales, sb, "uint8"),
-        ("out", out, desc.N * frames * desc.H * desc.W * desc.C, None)))
-    return _status(lib.ccv3d_qcache_read(ctypes.byref(desc), a[0], a[1], head, frames, a[2],
-                                         _stream(stream)), "ccv3d_qcache_read", check)
+    n = desc.N * frames * desc.H * desc.W * desc.C
+    a, st = _operands("ccv3d_qcache_read", desc.dtype, stream, (("out", out, n),),
+                      _ring(desc, codes, scales))
+    return _status(lib.ccv3d_qcache_read(desc, a[1], a[2], head, frames, a[0], st),
+                   "ccv3d_qcache_read", check)
 
 
 def ccv3d_forward_qring(plan, x, desc: ccv3d_qcache_desc, codes, scales, head: int, cache_buf, w,
                         bias, out, stride, pad, dilation, stream=None, check: bool = True):
     """ccv3d_forward_ring with the ring held in 8 or 4 bits.  Returns (status,
     next_head)."""
-    cb, sb = _ring_bytes(desc)
     dt = desc.dtype
-    a = _operands("ccv3d_forward_qring", dt, (
-        ("x", x, None, None), ("codes", codes, cb, "uint8"), ("scales", scales, sb, "uint8"),
-        ("cache_buf", cache_buf, None, None), ("w", w, None, None), ("bias", bias, None, None),
-        ("out", out, None, None)))
+    a, st = _operands("ccv3d_forward_qring", dt, stream, (), (
+        ("x", x, None, dt), *_ring(desc, codes, scales), ("cache_buf", cache_buf, None, dt),
+        ("w", w, None, dt), ("bias", bias, None, dt), ("out", out, None, dt)))
     s, p, d = (ctypes.c_int * 2)(*stride), (ctypes.c_int * 2)(*pad), (ctypes.c_int * 3)(*dilation)
     nh = ctypes.c_int(-1)
-    rc = lib.ccv3d_forward_qring(plan, a[0], ctypes.byref(desc), a[1], a[2], int(head), a[3], a[4],
-                                 a[5], a[6], s, p, d, _stream(stream), ctypes.byref(nh))
+    rc = lib.ccv3d_forward_qring(plan, a[0], desc, a[1], a[2], int(head), a[3], a[4], a[5], a[6],
+                                 s, p, d, st, ctypes.byref(nh))
     return _status(rc, "ccv3d_forward_qring", check), nh.value
 
 
