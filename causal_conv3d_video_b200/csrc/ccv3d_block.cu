@@ -254,7 +254,7 @@ ccv3d_status check_pointwise(const ccv3d_pointwise_desc* d) {
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Shape of a product on FFMA: tiles of 128, or of 64 where less of them is lost
-// at the edges or in the last wave (a 64-wide tile's time counts 1.4 times its
+// at the edges or in the last wave (a 64-wide tile's time counts 1.5 times its
 // share of a 128-wide one's: half the FMAs per shared-memory read), and splits of
 // the reduction while that leaves SMs without a block, of at least 8 steps of 16.
 struct SimtShape {
@@ -269,9 +269,9 @@ SimtShape simt_shape(long long M, long long N, long long K) {
         const int want = (int)std::max<long long>(1, std::min<long long>({2 * kSms / tiles, up(K, 128), 512}));
         const long long per = up(up(K, want), kPwK) * kPwK;
         const int splits = (int)std::max<long long>(1, up(K, per));
-        const int resident = t == 128 ? 2 : 4;  // blocks an SM, in equal shares of its time
-        const double c = std::ceil((double)tiles * splits / (kSms * resident)) * resident *
-                         (double)t * t * (per + 32) * (t == 128 ? 1.0 : 1.4);
+        // (blocks on one SM share its time: what counts is the fullest SM's share)
+        const double c = std::ceil((double)tiles * splits / kSms) * (double)t * t * (per + 32) *
+                         (t == 128 ? 1.0 : 1.5);
         if (c < cost) {
             cost = c;
             best = {t, splits, tiles, per};
@@ -577,6 +577,8 @@ ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb
     p.splits = s.splits;
     p.k_per_split = s.k_per_split;
     p.ldp = (int)up(N, 4) * 4;
+    p.a_elems = (AK ? M : K) * lda;
+    p.b_elems = (BK ? N : K) * ldb;
     p.o = o;
     p.o.partial = p.splits > 1 ? partial : nullptr;
     if (s.tiles > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;

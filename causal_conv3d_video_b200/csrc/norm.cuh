@@ -952,7 +952,8 @@ __device__ __forceinline__ void fin_sums(const float* src, long long slots, int 
         for (long long i = threadIdx.y; i < n; i += kFinRows)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                if (q < nq) s[q] += src[(q * slots + i * stride) * C + c];
+                if (q < nq && index_ok(&g_block_status, i * stride, slots))
+                    s[q] += src[(q * slots + i * stride) * C + c];
     }
     const int t = threadIdx.y * kFinCols + threadIdx.x;  // a warp: 4 rows of 8 columns
     __syncthreads();

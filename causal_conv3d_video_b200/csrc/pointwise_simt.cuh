@@ -26,6 +26,7 @@ struct PwSimt {
     long long M, K;
     int N, ldp, splits, vec;  // vec: rows of both operands are 16-byte multiples
     long long k_per_split;
+    long long a_elems, b_elems;  // extents of A and B (checked build)
     PwOut o;
 };
 
@@ -44,31 +45,45 @@ __device__ __forceinline__ void pw_store(const PwOut& o, long long m, int n, flo
 
 constexpr int kPwK = 16, kPwPad = 4;
 
-// A thread's part of an operand tile of R rows x 16 k: kV values along k (k-major
-// operand) or along the rows, at `p`, which moves on by 16 k a step.
+// A thread's part of an operand tile of R rows x 16 k: with 16-byte rows kV
+// values along the contiguous direction, otherwise kV single ones, 16 rows
+// apart, neighbouring threads along the contiguous direction (so that a warp's
+// load covers whole sectors).  The part moves on by 16 k a step.
 template <typename T, bool KMAJOR, int R>
 struct PwFetch {
     static constexpr int kV = R / 16, kPer = 16 / kV;  // kPer threads along a row's 16 k
     const T* p;
-    long long step;
-    int rows, k;  // rows there are from the thread's on (k-major: 0 or 1); its k in a step
+    long long step, next_row;
+    int rows, k;  // rows there are from the thread's on; its k in a step
     bool vec;
-    __device__ __forceinline__ PwFetch(const T* base, long long s_row, long long s_k,
-                                       long long row0, long long n_rows, long long k0, int tid,
-                                       bool v) {
-        const long long r = KMAJOR ? row0 + tid / kPer : row0 + (tid & 15) * kV;
-        k = KMAJOR ? tid % kPer * kV : tid >> 4;
+    const T* base_;
+    long long elems_;
+    __device__ __forceinline__ PwFetch(const T* base, long long elems, long long s_row,
+                                       long long s_k, long long row0, long long n_rows,
+                                       long long k0, int tid, bool v)
+        : vec(v), base_(base), elems_(elems) {
+        const int r = v ? (KMAJOR ? tid / kPer : (tid & 15) * kV) : (KMAJOR ? tid >> 4 : tid & 15);
+        k = v && KMAJOR ? tid % kPer * kV : (KMAJOR ? tid & 15 : tid >> 4);
         // (s_row = 1 or s_k = 1 along the contiguous direction)
-        p = base + (KMAJOR ? r * s_row + (k0 + k) : (k0 + k) * s_k + r);
-        step = KMAJOR ? kPwK : kPwK * s_k;
-        const long long left = n_rows - r;
-        rows = (int)(left <= 0 ? 0 : (left < kV ? left : kV));
-        vec = v && (KMAJOR || rows == kV);
+        const long long sr = KMAJOR ? s_row : 1, sk = KMAJOR ? 1 : s_k;
+        p = base + (row0 + r) * sr + (k0 + k) * sk;
+        step = kPwK * sk;
+        next_row = 16 * sr;
+        const long long left = n_rows - row0 - r;
+        rows = (int)(left <= 0 ? 0 : (left < R ? left : R));
+    }
+    __device__ __forceinline__ bool there(const T* q, int n) const {
+        return in_bounds(&g_block_status, q, n * (long long)sizeof(T), base_,
+                         elems_ * (long long)sizeof(T));
     }
     // The values of the next step, of which `left` k remain from its first on.
     __device__ __forceinline__ void operator()(float (&v)[kV], int left) {
-        const bool in = KMAJOR ? rows > 0 : left > k;
-        if (in && vec && (!KMAJOR || left >= k + kV)) {
+        if (!vec) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                v[i] = k < left && 16 * i < rows && there(p + i * next_row, 1)
+                           ? (float)p[i * next_row] : 0.0f;
+        } else if ((KMAJOR ? rows > 0 && left >= k + kV : left > k && rows >= kV) && there(p, kV)) {
 #pragma unroll
             for (int i = 0; i < kV; i += 4) {
                 const float4 x = *reinterpret_cast<const float4*>(p + i);
@@ -77,25 +92,26 @@ struct PwFetch {
         } else {
 #pragma unroll
             for (int i = 0; i < kV; ++i)
-                v[i] = in && (KMAJOR ? k + i < left : i < rows) ? (float)p[i] : 0.0f;
+                v[i] = (KMAJOR ? rows > 0 && k + i < left : k < left && i < rows) && there(p + i, 1)
+                           ? (float)p[i] : 0.0f;
         }
         p += step;
     }
-};
-
-template <bool KMAJOR, int R>
-__device__ __forceinline__ void pw_put(float (*s)[R + kPwPad], const float (&v)[R / 16], int tid) {
-    constexpr int kV = R / 16, kPer = 16 / kV;
-    if constexpr (KMAJOR) {
+    __device__ __forceinline__ void put(float (*s)[R + kPwPad], const float (&v)[kV], int tid) const {
+        if (!vec) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) s[tid % kPer * kV + i][tid / kPer] = v[i];
-    } else {
+            for (int i = 0; i < kV; ++i) s[k][(KMAJOR ? tid >> 4 : tid & 15) + 16 * i] = v[i];
+        } else if constexpr (KMAJOR) {
 #pragma unroll
-        for (int i = 0; i < kV; i += 4)
-            *reinterpret_cast<float4*>(&s[tid >> 4][(tid & 15) * kV + i]) =
-                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            for (int i = 0; i < kV; ++i) s[tid % kPer * kV + i][tid / kPer] = v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kV; i += 4)
+                *reinterpret_cast<float4*>(&s[tid >> 4][(tid & 15) * kV + i]) =
+                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
     }
-}
+};
 
 // S x S tile a block (S = 128 or 64), S/16 x S/16 values a thread, k in steps of
 // 16 through two shared-memory buffers; the next step's operands wait in
@@ -125,15 +141,15 @@ __global__ void __launch_bounds__(256, S == 128 ? 2 : 4) pw_simt_kernel(
 #pragma unroll
         for (int j = 0; j < kT / 2; ++j) acc[i][j] = f2_all(0.0f);
     float va[kT], vb[kT];
-    PwFetch<T, AK, S> fa(A, p.sam, p.sak, m0, p.M, kb, tid, p.vec);
-    PwFetch<T, BK, S> fb(B, p.sbn, p.sbk, n0, p.N, kb, tid, p.vec);
+    PwFetch<T, AK, S> fa(A, p.a_elems, p.sam, p.sak, m0, p.M, kb, tid, p.vec);
+    PwFetch<T, BK, S> fb(B, p.b_elems, p.sbn, p.sbk, n0, p.N, kb, tid, p.vec);
     int left = (int)(ke - kb);
     fa(va, left);
     fb(vb, left);
     int cur = 0;
     for (; left > 0; left -= kPwK, cur ^= 1) {
-        pw_put<AK, S>(sa[cur], va, tid);
-        pw_put<BK, S>(sb[cur], vb, tid);
+        fa.put(sa[cur], va, tid);
+        fb.put(sb[cur], vb, tid);
         __syncthreads();
         if (left > kPwK) {
             fa(va, left - kPwK);
@@ -188,7 +204,10 @@ __global__ void __launch_bounds__(256, S == 128 ? 2 : 4) pw_simt_kernel(
             float* dst = o.partial + ((long long)blockIdx.z * p.M + mh) * p.ldp + n;
 #pragma unroll 4
             for (int r = tid / S; r < 64; r += kStep)
-                if (mh + r < p.M) dst[(long long)r * p.ldp] = smem[r * S + tid % S];
+                if (mh + r < p.M &&
+                    in_bounds(&g_block_status, dst + (long long)r * p.ldp, 4, o.partial,
+                              (long long)p.splits * p.M * p.ldp * 4))
+                    dst[(long long)r * p.ldp] = smem[r * S + tid % S];
             continue;
         }
         const float b = bias != nullptr ? (float)bias[n] : 0.0f;
@@ -232,6 +251,9 @@ __global__ void __launch_bounds__(256) pw_join_kernel(const float* partial, int 
             b[j] = in && bias != nullptr ? (float)bias[n + j] : 0.0f;
         }
         const float* src = partial + m * ldp + n;
+        if (!in_bounds(&g_block_status, src + (splits - 1) * o.M * ldp, 16, partial,
+                       (long long)splits * o.M * ldp * 4))
+            continue;
 #pragma unroll 4
         for (int s = 0; s < splits; ++s) {
             const float4 x = *reinterpret_cast<const float4*>(src + s * o.M * ldp);
@@ -270,8 +292,12 @@ __global__ void __launch_bounds__(256) pw_rows_kernel(const T* x, const T* w, in
         Raw8<T, V> rw[CPW];
 #pragma unroll
         for (int c = 0; c < CPW; ++c) {
-            if (n0 + c < o.N) load8<T, V>(rw[c], w + (long long)(n0 + c) * K, c0, 32, K);
-            else zero8<T, V>(rw[c]);
+            const T* row = w + (long long)(n0 + c) * K;
+            if (n0 + c < o.N && in_bounds(&g_block_status, row, (long long)K * sizeof(T), w,
+                                          (long long)o.N * K * sizeof(T)))
+                load8<T, V>(rw[c], row, c0, 32, K);
+            else
+                zero8<T, V>(rw[c]);
         }
         f2 f[CPW][4];
 #pragma unroll
@@ -356,6 +382,8 @@ __global__ void __launch_bounds__(256) pw_rows_mma_kernel(const bf16_t* x, const
         for (int r = 0; r < 8; ++r) {
             // channels past the end read as the last one (and are not stored)
             const bf16_t* from = w + (long long)min(n0 + r, o.N - 1) * K + k0;
+            // checked build: a range outside w is recorded and read from its start
+            if (!in_bounds(&g_block_status, from, bytes, w, (long long)o.N * K * 2)) from = w;
             bulk_g2s(smem_u32(ring[c % kRwStages][r]), from, bytes, bar);
         }
     };
@@ -379,8 +407,9 @@ __global__ void __launch_bounds__(256) pw_rows_mma_kernel(const bf16_t* x, const
             const int k = c * kRwK + (u * 8 + warp) * 32 + t * 8;
 #pragma unroll
             for (int m = 0; m < kTiles * 2; ++m)
-                rx[u][m] = m < MB && k < K ? *reinterpret_cast<const uint4*>(xr[m < MB ? m : 0] + k)
-                                           : zero;
+                rx[u][m] = m < MB && k < K && in_bounds(&g_block_status, xr[m < MB ? m : 0] + k, 16,
+                                                        x, o.M * K * 2)
+                               ? *reinterpret_cast<const uint4*>(xr[m < MB ? m : 0] + k) : zero;
         }
         const int st = c % kRwStages;
         if (live && !mbar_wait(smem_u32(&full[st]), (uint32_t)(c / kRwStages & 1), &g_block_status,
@@ -445,7 +474,8 @@ __global__ void __launch_bounds__(256) pw_dact_kernel(const T* pre, const T* dou
             const long long at = r + (long long)j * rows;
             zero8<T, V>(rd[j]);
             zero8<T, V>(rp[j]);
-            if (at < r1) {
+            if (at < r1 && in_bounds(&g_block_status, dout + at * N, (long long)N * sizeof(T), dout,
+                                     M * N * (long long)sizeof(T))) {
                 load8<T, V>(rd[j], dout + at * N, c0, tpr, N);
                 if (pre != nullptr) load8<T, V>(rp[j], pre + at * N, c0, tpr, N);
             }
@@ -462,7 +492,10 @@ __global__ void __launch_bounds__(256) pw_dact_kernel(const T* pre, const T* dou
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] += d[i];
-            if (dp != nullptr && at < r1) store8<T, V>(pack8<T, V>(d), dp + at * ldp, c0, tpr, ldp);
+            if (dp != nullptr && at < r1 &&
+                in_bounds(&g_block_status, dp + at * ldp, (long long)ldp * sizeof(T), dp,
+                          M * ldp * (long long)sizeof(T)))
+                store8<T, V>(pack8<T, V>(d), dp + at * ldp, c0, tpr, ldp);
         }
     }
     if (colsum == nullptr) return;
@@ -473,7 +506,8 @@ __global__ void __launch_bounds__(256) pw_dact_kernel(const T* pre, const T* dou
         float a = 0.0f;
         for (int s = 0; s < rows; ++s) a += buf[s * tpr * 8 + j];
         const int l = j >> 3, i = j & 7, c = V ? cbase + l * 8 + i : cbase + l + i * tpr;
-        if (c < N) colsum[(long long)blockIdx.y * N + c] = a;
+        if (c < N && index_ok(&g_block_status, (long long)blockIdx.y * N + c, (long long)gridDim.y * N))
+            colsum[(long long)blockIdx.y * N + c] = a;
     }
 }
 

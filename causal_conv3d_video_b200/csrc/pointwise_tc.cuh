@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(256) pw_pack_kernel(const bf16_t* src, bf16_t*
         const int c0 = (int)(i - r * (Cp / 8)) * 8;
         Raw8<bf16_t, false> raw;
         float f[8];
+        if (!in_bounds(&g_block_status, src + r * C, C * 2LL, src, rows * C * 2)) continue;
         load8<bf16_t, false>(raw, src + r * C, c0, 1, C);
         unpack8<bf16_t, false>(raw, f);
         *reinterpret_cast<uint4*>(dst + r * Cp + c0) = pack8<bf16_t, true>(f).a;

@@ -133,3 +133,30 @@ def test_residual_block_streamed(fmt):
     assert err <= 5 * 2.0 ** -8 + step * (2.0 ** -8 / step) ** 0.5
     m = oracle.metrics(_np(out), _np(want))
     assert m["nonfinite"] == 0
+
+
+def test_block_suites_under_checked_build():
+    """The bounds-checked build (libccv3d_checked.so): the suites of the operators
+    around the convolution with every device address a kernel computes checked
+    against its buffer.  Their far-offset tests are left to the normal build."""
+    import os
+    import subprocess
+    import sys
+    if os.environ.get("CCV3D_LIBRARY") == "checked":
+        pytest.skip("already running on it")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run(
+        [sys.executable, "-m", "pytest", "-q", "-m", "gpu", "-p", "no:cacheprovider",
+         "tests/test_gpu_norm.py", "tests/test_gpu_pointwise.py", "tests/test_gpu_qcache.py",
+         "tests/test_gpu_block.py", "-k", "not far"],
+        cwd=root, env=dict(os.environ, CCV3D_LIBRARY="checked"), capture_output=True, text=True,
+        timeout=1200)
+    tail = (r.stdout + r.stderr)[-3000:]
+    assert r.returncode == 0 and " passed" in r.stdout, tail
+
+
+@pytest.fixture(autouse=True)
+def status_is_clean():
+    """No call of a test left an error in the library's status word."""
+    yield
+    assert ccv3d.ccv3d_block_get_status() == ccv3d.CCV3D_OK

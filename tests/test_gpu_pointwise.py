@@ -268,3 +268,11 @@ def test_far_pixels():
     close(out[-3:], want, HALF["bf16"] * want.abs() + _acc(N) * mag, "dx")
     assert int((out[:-3] != 0).sum()) == 0
     assert ccv3d.ccv3d_block_get_status() == ccv3d.CCV3D_OK
+
+
+@pytest.fixture(autouse=True)
+def status_is_clean():
+    """No call of a test left an error (a wait that ran out; in the checked build
+    an address outside its buffer) in the library's status word."""
+    yield
+    assert ccv3d.ccv3d_block_get_status() == ccv3d.CCV3D_OK
