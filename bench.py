@@ -25,6 +25,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -70,11 +71,19 @@ def load_peaks():
 
 
 def kernel_source_digest():
-    h = hashlib.sha256()
+    """Digest of the convolution's sources: ccv3d.cu and what it includes of csrc."""
     csrc = os.path.join(ROOT, "causal_conv3d_video_b200", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    sources, todo = {}, ["ccv3d.cu"]
+    while todo:
+        name = todo.pop()
+        if name in sources or not os.path.exists(os.path.join(csrc, name)):
+            continue
         with open(os.path.join(csrc, name), "rb") as f:
-            h.update(name.encode() + f.read())
+            sources[name] = f.read()
+        todo += re.findall(r'#include "([^"]+)"', sources[name].decode())
+    h = hashlib.sha256()
+    for name in sorted(sources):
+        h.update(name.encode() + sources[name])
     return h.hexdigest()[:16]
 
 

@@ -253,28 +253,30 @@ ccv3d_status check_pointwise(const ccv3d_pointwise_desc* d) {
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Shape of a product on FFMA: tiles of 128, or of 64 where less of them is lost
-// at the edges or in the last wave (a 64-wide tile's time counts 1.5 times its
-// share of a 128-wide one's: half the FMAs per shared-memory read), and splits of
-// the reduction while that leaves SMs without a block, of at least 8 steps of 16.
+// Shape of a product on FFMA: tiles of 128 x 128, or of 64 x 64 or 128 x 32
+// where less of them is lost at the edges or in the last wave (their values
+// count 1.5 times a 128 x 128 tile's: half the FMAs per shared-memory read), and
+// splits of the reduction while that leaves SMs without a block, of at least 8
+// steps of 16.
 struct SimtShape {
-    int tile, splits;
+    int tm, tn, splits;
     long long tiles, k_per_split;
 };
 SimtShape simt_shape(long long M, long long N, long long K) {
+    constexpr int kTiles[3][2] = {{128, 128}, {64, 64}, {128, 32}};
     SimtShape best = {};
     double cost = 1e300;
-    for (int t : {128, 64}) {
-        const long long tiles = up(M, t) * up(N, t);
+    for (const auto& t : kTiles) {
+        const long long tiles = up(M, t[0]) * up(N, t[1]);
         const int want = (int)std::max<long long>(1, std::min<long long>({2 * kSms / tiles, up(K, 128), 512}));
         const long long per = up(up(K, want), kPwK) * kPwK;
         const int splits = (int)std::max<long long>(1, up(K, per));
         // (blocks on one SM share its time: what counts is the fullest SM's share)
-        const double c = std::ceil((double)tiles * splits / kSms) * (double)t * t * (per + 32) *
-                         (t == 128 ? 1.0 : 1.5);
+        const double c = std::ceil((double)tiles * splits / kSms) * (double)t[0] * t[1] * (per + 32) *
+                         (t[1] == 128 ? 1.0 : 1.5);
         if (c < cost) {
             cost = c;
-            best = {t, splits, tiles, per};
+            best = {t[0], t[1], splits, tiles, per};
         }
     }
     return best;
@@ -583,8 +585,9 @@ ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb
     p.o.partial = p.splits > 1 ? partial : nullptr;
     if (s.tiles > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)s.tiles, 1, p.splits);
-    if (s.tile == 128) pw_simt_kernel<float, AK, BK, 128><<<grid, 256, 0, st>>>(p);
-    else pw_simt_kernel<float, AK, BK, 64><<<grid, 256, 0, st>>>(p);
+    if (s.tn == 128) pw_simt_kernel<float, AK, BK, 128, 128><<<grid, 256, 0, st>>>(p);
+    else if (s.tn == 64) pw_simt_kernel<float, AK, BK, 64, 64><<<grid, 256, 0, st>>>(p);
+    else pw_simt_kernel<float, AK, BK, 128, 32><<<grid, 256, 0, st>>>(p);
     if (p.splits > 1) {
         const long long blocks = std::min<long long>(up(M * (p.ldp / 4), 256), kSms * 16LL);
         pw_join_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(partial, p.splits, p.ldp, o);
@@ -700,7 +703,7 @@ ccv3d_status check_qcache(const ccv3d_qcache_desc* d) {
         return CCV3D_ERR_INVALID;
     if (d->C > 65536 || (long long)d->H * d->W > 0x7fffffffLL ||
         (long long)d->N * d->ring_slots > 0x7fffffffLL ||
-        (double)d->N * d->ring_slots * d->H * d->W * d->C > 7e13)
+        (double)d->N * d->ring_slots * d->H * d->W * d->C > 1e13)
         return CCV3D_ERR_UNSUPPORTED;
     return CCV3D_OK;
 }
@@ -725,16 +728,20 @@ dim3 qcache_grid(const QCacheJob& j, long long threads_a_pixel) {
 template <typename T>
 void qcache_write_run(const QCacheJob& j, int fmt, cudaStream_t st) {
     const dim3 grid = qcache_grid(j, 4LL * j.groups);
-    if (j.C % 32 == 0) qcache_write_kernel<T, true, true><<<grid, kQThreads, 0, st>>>(j, fmt);
-    else if (j.C % 8 == 0) qcache_write_kernel<T, true, false><<<grid, kQThreads, 0, st>>>(j, fmt);
-    else qcache_write_kernel<T, false, false><<<grid, kQThreads, 0, st>>>(j, fmt);
+    if (j.C % 32 == 0) qcache_write_kernel<T, 8, true><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else if (j.C % 8 == 0) qcache_write_kernel<T, 8, false><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else if (j.C % 4 == 0) qcache_write_kernel<T, 4, false><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else if (j.C % 2 == 0) qcache_write_kernel<T, 2, false><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else qcache_write_kernel<T, 1, false><<<grid, kQThreads, 0, st>>>(j, fmt);
 }
 template <typename T>
 void qcache_read_run(const QCacheJob& j, int fmt, cudaStream_t st) {
     const dim3 grid = qcache_grid(j, up(j.C, 8));
-    if (j.C % 32 == 0) qcache_read_kernel<T, true, true><<<grid, kQThreads, 0, st>>>(j, fmt);
-    else if (j.C % 8 == 0) qcache_read_kernel<T, true, false><<<grid, kQThreads, 0, st>>>(j, fmt);
-    else qcache_read_kernel<T, false, false><<<grid, kQThreads, 0, st>>>(j, fmt);
+    if (j.C % 32 == 0) qcache_read_kernel<T, 8, true><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else if (j.C % 8 == 0) qcache_read_kernel<T, 8, false><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else if (j.C % 4 == 0) qcache_read_kernel<T, 4, false><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else if (j.C % 2 == 0) qcache_read_kernel<T, 2, false><<<grid, kQThreads, 0, st>>>(j, fmt);
+    else qcache_read_kernel<T, 1, false><<<grid, kQThreads, 0, st>>>(j, fmt);
 }
 
 }  // namespace

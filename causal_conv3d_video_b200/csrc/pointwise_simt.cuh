@@ -51,7 +51,8 @@ constexpr int kPwK = 16, kPwPad = 4;
 // load covers whole sectors).  The part moves on by 16 k a step.
 template <typename T, bool KMAJOR, int R>
 struct PwFetch {
-    static constexpr int kV = R / 16, kPer = 16 / kV;  // kPer threads along a row's 16 k
+    // kPer threads along a row's 16 k (parts of under four values go singly: vec is false)
+    static constexpr int kV = R / 16, kPer = 16 / kV;
     const T* p;
     long long step, next_row;
     int rows, k;  // rows there are from the thread's on; its k in a step
@@ -83,9 +84,10 @@ struct PwFetch {
             for (int i = 0; i < kV; ++i)
                 v[i] = k < left && 16 * i < rows && there(p + i * next_row, 1)
                            ? (float)p[i * next_row] : 0.0f;
-        } else if ((KMAJOR ? rows > 0 && left >= k + kV : left > k && rows >= kV) && there(p, kV)) {
+        } else if (kV % 4 == 0 && (KMAJOR ? rows > 0 && left >= k + kV : left > k && rows >= kV) &&
+                   there(p, kV)) {
 #pragma unroll
-            for (int i = 0; i < kV; i += 4) {
+            for (int i = 0; i + 3 < kV; i += 4) {
                 const float4 x = *reinterpret_cast<const float4*>(p + i);
                 v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
             }
@@ -106,43 +108,48 @@ struct PwFetch {
             for (int i = 0; i < kV; ++i) s[tid % kPer * kV + i][tid / kPer] = v[i];
         } else {
 #pragma unroll
-            for (int i = 0; i < kV; i += 4)
+            for (int i = 0; i + 3 < kV; i += 4)
                 *reinterpret_cast<float4*>(&s[tid >> 4][(tid & 15) * kV + i]) =
                     make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
     }
 };
 
-// S x S tile a block (S = 128 or 64), S/16 x S/16 values a thread, k in steps of
-// 16 through two shared-memory buffers; the next step's operands wait in
-// registers.  128 has the better ratio of FMAs to shared-memory reads; 64 is
-// for products whose edges or few tiles would idle much of it.
-template <typename T, bool AK, bool BK, int S>
-__global__ void __launch_bounds__(256, S == 128 ? 2 : 4) pw_simt_kernel(
+// SM x SN tile a block (128 x 128, 64 x 64 or 128 x 32), k in steps of 16
+// through two shared-memory buffers; the next step's operands wait in
+// registers.  A thread has 4 rows by 4 columns of each SM/GM x SN/GN part.  The
+// largest has the best ratio of FMAs to shared-memory reads, the others are for
+// products whose edges or few tiles would idle much of it.
+template <typename T, bool AK, bool BK, int SM, int SN>
+__global__ void __launch_bounds__(256, SM * SN == 128 * 128 ? 2 : 4) pw_simt_kernel(
     const __grid_constant__ PwSimt p) {
-    constexpr int kT = S / 16, kH = kT / 4;
-    typedef float Slab[2][kPwK][S + kPwPad];
-    __shared__ __align__(16) float smem[2 * 2 * kPwK * (S + kPwPad)];
-    Slab& sa = *reinterpret_cast<Slab*>(smem);
-    Slab& sb = *reinterpret_cast<Slab*>(smem + 2 * kPwK * (S + kPwPad));
-    static_assert(64 * S <= 2 * 2 * kPwK * (S + kPwPad), "half a tile fits the operands' buffers");
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int tiles_n = (p.N + S - 1) / S;
+    constexpr int kTx = SN >= 64 ? 16 : 8, kTy = 256 / kTx;  // threads across and down
+    constexpr int kHm = SM / (kTy * 4), kHn = SN / (kTx * 4);
+    constexpr int kA = 2 * kPwK * (SM + kPwPad), kB = 2 * kPwK * (SN + kPwPad);
+    typedef float SlabA[2][kPwK][SM + kPwPad];
+    typedef float SlabB[2][kPwK][SN + kPwPad];
+    __shared__ __align__(16) float smem[kA + kB];
+    SlabA& sa = *reinterpret_cast<SlabA*>(smem);
+    SlabB& sb = *reinterpret_cast<SlabB*>(smem + kA);
+    constexpr int kGm = kTy * 4, kGn = kTx * 4;  // rows and columns of a part
+    static_assert(kGm * SN <= kA + kB, "a row of parts fits the operands' buffers");
+    const int tid = threadIdx.x, tx = tid % kTx, ty = tid / kTx;
+    const int tiles_n = (p.N + SN - 1) / SN;
     const long long tile = blockIdx.x;
-    const long long m0 = tile / tiles_n * S;
-    const int n0 = (int)(tile % tiles_n) * S;
+    const long long m0 = tile / tiles_n * SM;
+    const int n0 = (int)(tile % tiles_n) * SN;
     const long long kb = (long long)blockIdx.z * p.k_per_split;
     const long long ke = kb + p.k_per_split < p.K ? kb + p.k_per_split : p.K;
     const T *A = static_cast<const T*>(p.A), *B = static_cast<const T*>(p.B);
     // accumulators and b values as pairs: one instruction, two FMAs
-    f2 acc[kT][kT / 2];
+    f2 acc[kHm * 4][kHn * 2];
 #pragma unroll
-    for (int i = 0; i < kT; ++i)
+    for (int i = 0; i < kHm * 4; ++i)
 #pragma unroll
-        for (int j = 0; j < kT / 2; ++j) acc[i][j] = f2_all(0.0f);
-    float va[kT], vb[kT];
-    PwFetch<T, AK, S> fa(A, p.a_elems, p.sam, p.sak, m0, p.M, kb, tid, p.vec);
-    PwFetch<T, BK, S> fb(B, p.b_elems, p.sbn, p.sbk, n0, p.N, kb, tid, p.vec);
+        for (int j = 0; j < kHn * 2; ++j) acc[i][j] = f2_all(0.0f);
+    float va[SM / 16], vb[SN / 16];
+    PwFetch<T, AK, SM> fa(A, p.a_elems, p.sam, p.sak, m0, p.M, kb, tid, p.vec);
+    PwFetch<T, BK, SN> fb(B, p.b_elems, p.sbn, p.sbk, n0, p.N, kb, tid, p.vec && SN >= 64);
     int left = (int)(ke - kb);
     fa(va, left);
     fb(vb, left);
@@ -157,28 +164,31 @@ __global__ void __launch_bounds__(256, S == 128 ? 2 : 4) pw_simt_kernel(
         }
 #pragma unroll
         for (int kk = 0; kk < kPwK; ++kk) {
-            float a[kT];
-            f2 b[kT / 2];
+            float a[kHm * 4];
+            f2 b[kHn * 2];
 #pragma unroll
-            for (int h = 0; h < kH; ++h) {
-                const float4 x = *reinterpret_cast<const float4*>(&sa[cur][kk][h * 64 + ty * 4]);
-                const ulonglong2 y =
-                    *reinterpret_cast<const ulonglong2*>(&sb[cur][kk][h * 64 + tx * 4]);
+            for (int h = 0; h < kHm; ++h) {
+                const float4 x = *reinterpret_cast<const float4*>(&sa[cur][kk][h * kGm + ty * 4]);
                 a[h * 4] = x.x; a[h * 4 + 1] = x.y; a[h * 4 + 2] = x.z; a[h * 4 + 3] = x.w;
+            }
+#pragma unroll
+            for (int h = 0; h < kHn; ++h) {
+                const ulonglong2 y =
+                    *reinterpret_cast<const ulonglong2*>(&sb[cur][kk][h * kGn + tx * 4]);
                 b[h * 2] = y.x;
                 b[h * 2 + 1] = y.y;
             }
 #pragma unroll
-            for (int i = 0; i < kT; ++i) {
+            for (int i = 0; i < kHm * 4; ++i) {
                 const f2 a2 = f2_all(a[i]);
 #pragma unroll
-                for (int j = 0; j < kT / 2; ++j) acc[i][j] = f2_fma(a2, b[j], acc[i][j]);
+                for (int j = 0; j < kHn * 2; ++j) acc[i][j] = f2_fma(a2, b[j], acc[i][j]);
             }
         }
         // (one barrier a step: the next step writes the other buffer, whose
         // readers passed this step's barrier)
     }
-    // Epilogue, 64 rows of the tile at a time through shared memory: the loop over
+    // Epilogue, a row of parts at a time through shared memory: the loop over
     // its values is then short (unrolled over the accumulators it outgrew the
     // instruction cache) and runs along the rows of out.  Four values' residuals
     // are read before their stores: out may be the residual, so the compiler
@@ -187,32 +197,32 @@ __global__ void __launch_bounds__(256, S == 128 ? 2 : 4) pw_simt_kernel(
     const T *bias = static_cast<const T*>(o.bias), *residual = static_cast<const T*>(o.residual);
     const long long bytes = o.M * o.N * (long long)sizeof(T);
 #pragma unroll
-    for (int h = 0; h < kH; ++h) {
+    for (int h = 0; h < kHm; ++h) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int g = 0; g < kH; ++g)
-                *reinterpret_cast<ulonglong2*>(&smem[(ty * 4 + i) * S + g * 64 + tx * 4]) =
+            for (int g = 0; g < kHn; ++g)
+                *reinterpret_cast<ulonglong2*>(&smem[(ty * 4 + i) * SN + g * kGn + tx * 4]) =
                     make_ulonglong2(acc[h * 4 + i][g * 2], acc[h * 4 + i][g * 2 + 1]);
         __syncthreads();
-        const long long mh = m0 + h * 64;
-        const int n = n0 + tid % S;  // (256 is a multiple of S: a thread's column)
+        const long long mh = m0 + h * kGm;
+        const int n = n0 + tid % SN;  // (256 is a multiple of SN: a thread's column)
         if (n >= p.N) continue;
-        constexpr int kStep = 256 / S;  // rows a pass
+        constexpr int kStep = 256 / SN;  // rows a pass
         if (o.partial != nullptr) {
             float* dst = o.partial + ((long long)blockIdx.z * p.M + mh) * p.ldp + n;
 #pragma unroll 4
-            for (int r = tid / S; r < 64; r += kStep)
+            for (int r = tid / SN; r < kGm; r += kStep)
                 if (mh + r < p.M &&
                     in_bounds(&g_block_status, dst + (long long)r * p.ldp, 4, o.partial,
                               (long long)p.splits * p.M * p.ldp * 4))
-                    dst[(long long)r * p.ldp] = smem[r * S + tid % S];
+                    dst[(long long)r * p.ldp] = smem[r * SN + tid % SN];
             continue;
         }
         const float b = bias != nullptr ? (float)bias[n] : 0.0f;
 #pragma unroll 1
-        for (int r = tid / S; r < 64; r += 4 * kStep) {
+        for (int r = tid / SN; r < kGm; r += 4 * kStep) {
             float res[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -224,7 +234,7 @@ __global__ void __launch_bounds__(256, S == 128 ? 2 : 4) pw_simt_kernel(
                 const long long m = mh + r + j * kStep;
                 T* out = static_cast<T*>(o.out) + m * o.N + n;
                 if (m >= p.M || !in_bounds(&g_block_status, out, sizeof(T), o.out, bytes)) continue;
-                const float u = smem[(r + j * kStep) * S + tid % S] + b;
+                const float u = smem[(r + j * kStep) * SN + tid % SN] + b;
                 if (o.pre != nullptr) static_cast<T*>(o.pre)[m * o.N + n] = (T)u;
                 *out = (T)(act_of<T>(u, o.act) + res[j]);
             }

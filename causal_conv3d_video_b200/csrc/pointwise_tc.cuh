@@ -214,6 +214,48 @@ __device__ __forceinline__ void pt_ahead(const PtParams& p, const PtShared& sh, 
     }
 }
 
+// A chunk of 32 rows between a staging buffer and a matrix whose rows are no
+// multiple of 16 bytes (no tensor map): row by row with the lanes along the
+// columns, two columns a lane where rows start on 4 bytes; several rows' reads
+// before their writes.
+template <int kCh, bool kLoad>
+__device__ __forceinline__ void pt_direct(const bf16_t* src, bf16_t* dst, uint8_t* buf,
+                                          const PtParams& p, int r0, int c0, bool in, int lane) {
+    constexpr int kRowB = kCh * 2;
+    const bf16_t* base = kLoad ? src : dst;
+    const long long bytes = p.M * p.N * 2;
+    const int rows = in ? (int)min(32LL, p.M - r0) : 0;
+    auto at = [&](int r, int c) { return buf + r * kRowB + (swizzled_chunk<kRowB>(c >> 3, r) << 4) + (c & 7) * 2; };
+    if ((p.N & 1) == 0) {
+        constexpr int kLanes = kCh / 2, kRows = 32 / kLanes;  // rows side by side in a warp
+        const int c = lane % kLanes * 2, sub = lane / kLanes;
+        if (c0 + c >= p.N) return;
+#pragma unroll 8
+        for (int r = sub; r < 32; r += kRows) {
+            const long long i = ((long long)r0 + r) * p.N + c0 + c;
+            const bool ok = r < rows && in_bounds(&g_block_status, base + i, 4, base, bytes);
+            if constexpr (kLoad)
+                *reinterpret_cast<uint32_t*>(at(r, c)) =
+                    ok ? *reinterpret_cast<const uint32_t*>(src + i) : 0u;
+            else if (ok)
+                *reinterpret_cast<uint32_t*>(dst + i) = *reinterpret_cast<const uint32_t*>(at(r, c));
+        }
+    } else {
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r)
+#pragma unroll
+            for (int c = lane; c < kCh; c += 32) {
+                const long long i = ((long long)r0 + r) * p.N + c0 + c;
+                const bool ok = r < rows && c0 + c < p.N &&
+                                in_bounds(&g_block_status, base + i, 2, base, bytes);
+                if constexpr (kLoad)
+                    *reinterpret_cast<bf16_t*>(at(r, c)) = ok ? src[i] : bf16_t(0.0f);
+                else if (ok)
+                    dst[i] = *reinterpret_cast<const bf16_t*>(at(r, c));
+            }
+    }
+}
+
 // The epilogue of one warp: every second chunk of kCh columns of its 32 rows.
 // kPart: chunks of 32 columns go out as fp32 partials.
 template <int kCh, bool kPart>
@@ -325,17 +367,8 @@ __device__ __forceinline__ void pt_epilogue(const PtParams& p, const PtShared& s
                                          p.wait_limit_ns))
                         ok = false;
                     src = sh.res + (size_t)(slot * 4 + q) * kBuf;
-                } else {  // row by row, lanes along the columns
-                    for (int r = 0; r < 32; ++r)
-#pragma unroll
-                        for (int i = lane; i < kCh; i += 32) {
-                            const long long at = (long long)r0 + r;
-                            *reinterpret_cast<bf16_t*>(buf + r * kRowB +
-                                                       (swizzled_chunk<kRowB>(i >> 3, r) << 4) +
-                                                       (i & 7) * 2) =
-                                in && at < p.M && c0 + i < p.N ? p.residual[at * p.N + c0 + i]
-                                                               : bf16_t(0.0f);
-                        }
+                } else {
+                    pt_direct<kCh, true>(p.residual, nullptr, buf, p, r0, c0, in, lane);
                     __syncwarp();
                 }
                 Raw8<bf16_t, true> res[kCh / 8];
@@ -377,17 +410,9 @@ __device__ __forceinline__ void pt_epilogue(const PtParams& p, const PtShared& s
                 }
             } else {
                 __syncwarp();
-                for (int r = 0; r < 32; ++r)
-#pragma unroll
-                    for (int i = lane; i < kCh; i += 32) {
-                        const long long at_r = (long long)r0 + r, at = at_r * p.N + c0 + i;
-                        if (!in || !ok || at_r >= p.M || c0 + i >= p.N) continue;
-                        const int off =
-                            r * kRowB + (swizzled_chunk<kRowB>(i >> 3, r) << 4) + (i & 7) * 2;
-                        if (!in_bounds(&g_block_status, p.out + at, 2, p.out, p.M * p.N * 2)) continue;
-                        p.out[at] = *reinterpret_cast<const bf16_t*>(buf + off);
-                        if (p.pre != nullptr) p.pre[at] = *reinterpret_cast<const bf16_t*>(pre + off);
-                    }
+                pt_direct<kCh, false>(nullptr, p.out, buf, p, r0, c0, in && ok, lane);
+                if (p.pre != nullptr)
+                    pt_direct<kCh, false>(nullptr, p.pre, pre, p, r0, c0, in && ok, lane);
                 __syncwarp();
             }
             turn ^= 1;

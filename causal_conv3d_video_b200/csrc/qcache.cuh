@@ -115,15 +115,124 @@ __device__ __forceinline__ void decode8(uint2 w, int c, int fmt, float (&x)[8]) 
 constexpr int kQUnits = 4;
 constexpr int kQThreads = 256;
 
+// Eight consecutive values from p on, of which `n` (or more) are there, in
+// loads of W values (the rows' and so p's alignment); the others are 0.
+template <typename T, int W>
+__device__ __forceinline__ void load_w(float (&x)[8], const T* p, int n) {
+    if constexpr (W == 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i < n ? (float)p[i] : 0.0f;
+    } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; i += W) {
+            uint32_t w[W / 2];
+            if constexpr (W == 2) {
+                w[0] = i < n ? *reinterpret_cast<const uint32_t*>(p + i) : 0u;
+            } else {
+                const uint2 t = i < n ? *reinterpret_cast<const uint2*>(p + i) : make_uint2(0u, 0u);
+                w[0] = t.x;
+                w[1] = t.y;
+            }
+#pragma unroll
+            for (int j = 0; j < W / 2; ++j) {
+                x[i + 2 * j] = lo_f(w[j]);
+                x[i + 2 * j + 1] = hi_f(w[j]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i += W) {
+            if constexpr (W == 2) {
+                const float2 t = i < n ? *reinterpret_cast<const float2*>(p + i) : make_float2(0.f, 0.f);
+                x[i] = t.x;
+                x[i + 1] = t.y;
+            } else {
+                const float4 t = i < n ? *reinterpret_cast<const float4*>(p + i)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[i] = t.x; x[i + 1] = t.y; x[i + 2] = t.z; x[i + 3] = t.w;
+            }
+        }
+    }
+}
+template <typename T, int W>
+__device__ __forceinline__ void store_w(const float (&x)[8], T* p, int n) {
+#pragma unroll
+    for (int i = 0; i < 8; i += W) {
+        if (i >= n) continue;
+        if constexpr (W == 1) {
+            p[i] = (T)x[i];
+        } else if constexpr (sizeof(T) == 2) {
+            if constexpr (W == 2) *reinterpret_cast<uint32_t*>(p + i) = pack_bf16(x[i], x[i + 1]);
+            else *reinterpret_cast<uint2*>(p + i) = make_uint2(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]));
+        } else {
+            if constexpr (W == 2) *reinterpret_cast<float2*>(p + i) = make_float2(x[i], x[i + 1]);
+            else *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        }
+    }
+}
+// The code bytes of eight values (`n` of them there) to or from a row of codes
+// whose pieces of W values are aligned; one byte a value, or half of one.
+template <int W>
+__device__ __forceinline__ void put_codes(uint2 w, uint8_t* p, int n, bool half) {
+    if (half) {
+        const int m = (n + 1) / 2;  // bytes
+        if constexpr (W == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2)
+                if (i < m) *reinterpret_cast<uint16_t*>(p + i) = (uint16_t)(w.x >> (8 * i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < m) p[i] = (uint8_t)(w.x >> (8 * i));
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i += W) {
+        const uint32_t v = (i < 4 ? w.x : w.y) >> (8 * (i & 3));
+        if (i >= n) continue;
+        if constexpr (W == 4) *reinterpret_cast<uint32_t*>(p + i) = v;
+        else if constexpr (W == 2) *reinterpret_cast<uint16_t*>(p + i) = (uint16_t)v;
+        else p[i] = (uint8_t)v;
+    }
+}
+template <int W>
+__device__ __forceinline__ uint2 get_codes(const uint8_t* p, int n, bool half) {
+    uint2 w = make_uint2(0u, 0u);
+    if (half) {
+        const int m = (n + 1) / 2;
+        if constexpr (W == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2)
+                if (i < m) w.x |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + i) << (8 * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < m) w.x |= (uint32_t)p[i] << (8 * i);
+        }
+        return w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i += W) {
+        if (i >= n) continue;
+        uint32_t v;
+        if constexpr (W == 4) v = *reinterpret_cast<const uint32_t*>(p + i);
+        else if constexpr (W == 2) v = *reinterpret_cast<const uint16_t*>(p + i);
+        else v = p[i];
+        (i < 4 ? w.x : w.y) |= v << (8 * (i & 3));
+    }
+    return w;
+}
+
 // Where unit u of a frame lies: its pixel, eight-channel unit of the pixel.
 struct QPlace {
     long long px;
     int r;
 };
 
-// blockIdx.y = n * frames + i; V: the channel count is a multiple of 8, kFlat:
-// of 32.
-template <typename T, bool V, bool kFlat>
+// blockIdx.y = n * frames + i; W: values a load, 8, 4, 2 or 1, which divides the
+// channel count; kFlat: 32 divides it.
+template <typename T, int W, bool kFlat>
 __global__ void __launch_bounds__(kQThreads) qcache_write_kernel(const __grid_constant__ QCacheJob p,
                                                                  int fmt) {
     const int n = blockIdx.y / p.frames, i = blockIdx.y - n * p.frames;
@@ -137,8 +246,17 @@ __global__ void __launch_bounds__(kQThreads) qcache_write_kernel(const __grid_co
     const int per = p.groups * 4;  // threads a pixel
     const long long units = p.pixels * per;
     const long long u0 = (long long)blockIdx.x * (kQThreads * kQUnits) + threadIdx.x;
-    Raw8<T, V> raw[kQUnits];
+    float x[kQUnits][8];
     QPlace at[kQUnits];
+    auto fetch = [&](float (&v)[8], const T* q, int n) {  // (n <= 0: past the pixel's channels)
+        if constexpr (W == 8) {
+            Raw8<T, true> raw;
+            load8<T, true>(raw, q, 0, 1, n);
+            unpack8<T, true>(raw, v);
+        } else {
+            load_w<T, W>(v, q, n);
+        }
+    };
 #pragma unroll
     for (int k = 0; k < kQUnits; ++k) {
         const long long u = u0 + k * kQThreads;
@@ -147,19 +265,17 @@ __global__ void __launch_bounds__(kQThreads) qcache_write_kernel(const __grid_co
         const T* row = kFlat ? src + u * 8 : src + at[k].px * p.C;
         const bool in = u < units;
         if (in && in_bounds(&g_block_status, row, (kFlat ? 8 : p.C) * (long long)sizeof(T), p.src, x_bytes))
-            load8<T, V>(raw[k], row, at[k].r * 8, 1, kFlat ? 8 : p.C);
+            fetch(x[k], row + at[k].r * 8, kFlat ? 8 : p.C - at[k].r * 8);
         else
-            zero8<T, V>(raw[k]);
+            for (int j = 0; j < 8; ++j) x[k][j] = 0.0f;
     }
 #pragma unroll
     for (int k = 0; k < kQUnits; ++k) {
         const long long u = u0 + k * kQThreads;
-        float x[8];
-        unpack8<T, V>(raw[k], x);
         // magnitudes as integers, whose order is the floats' and puts NaN on top
         uint32_t a = 0u;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(x[j]) & 0x7fffffffu);
+        for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(x[k][j]) & 0x7fffffffu);
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
         const int c = a == 0u ? 1 : scale_byte(__uint_as_float(a), fmt);
@@ -168,29 +284,22 @@ __global__ void __launch_bounds__(kQThreads) qcache_write_kernel(const __grid_co
         uint8_t* sc = kFlat ? scales + (u >> 2) : scales + at[k].px * p.groups + (at[k].r >> 2);
         if ((threadIdx.x & 3) == 0 && in_bounds(&g_block_status, sc, 1, p.scales, s_bytes))
             *sc = (uint8_t)c;
-        const uint2 w = encode8(x, c, fmt);
-        if constexpr (kFlat) {
-            if (fmt == kQE2m1) *reinterpret_cast<uint32_t*>(codes + u * 4) = w.x;
-            else *reinterpret_cast<uint2*>(codes + u * 8) = w;
-        } else {
-            uint8_t* out = codes + at[k].px * p.code_bytes;
-            if constexpr (V) {
-                if (c0 < p.C) {
-                    if (fmt == kQE2m1) *reinterpret_cast<uint32_t*>(out + c0 / 2) = w.x;
-                    else *reinterpret_cast<uint2*>(out + c0) = w;
-                }
-            } else if (fmt == kQE2m1) {
-                for (int j = 0; j < 4; ++j)
-                    if (c0 / 2 + j < p.code_bytes) out[c0 / 2 + j] = (uint8_t)(w.x >> (8 * j));
-            } else {
-                for (int j = 0; j < 8; ++j)
-                    if (c0 + j < p.C) out[c0 + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+        const uint2 w = encode8(x[k], c, fmt);
+        if constexpr (W == 8) {
+            uint8_t* out = kFlat ? codes : codes + at[k].px * p.code_bytes;
+            const long long o = kFlat ? u * 8 : c0;
+            if (kFlat || c0 < p.C) {
+                if (fmt == kQE2m1) *reinterpret_cast<uint32_t*>(out + o / 2) = w.x;
+                else *reinterpret_cast<uint2*>(out + o) = w;
             }
+        } else if (c0 < p.C) {
+            uint8_t* out = codes + at[k].px * p.code_bytes + (fmt == kQE2m1 ? c0 / 2 : c0);
+            put_codes<W>(w, out, p.C - c0, fmt == kQE2m1);
         }
     }
 }
 
-template <typename T, bool V, bool kFlat>
+template <typename T, int W, bool kFlat>
 __global__ void __launch_bounds__(kQThreads) qcache_read_kernel(const __grid_constant__ QCacheJob p,
                                                                 int fmt) {
     const int n = blockIdx.y / p.frames, i = blockIdx.y - n * p.frames;
@@ -220,18 +329,12 @@ __global__ void __launch_bounds__(kQThreads) qcache_read_kernel(const __grid_con
         ok[k] = u < units && in_bounds(&g_block_status, sc, 1, p.scales, s_bytes);
         if (!ok[k]) continue;
         c[k] = *sc;
-        if constexpr (kFlat) {
-            if (fmt == kQE2m1) w[k].x = *reinterpret_cast<const uint32_t*>(codes + u * 4);
-            else w[k] = *reinterpret_cast<const uint2*>(codes + u * 8);
-        } else if constexpr (V) {
-            if (fmt == kQE2m1) w[k].x = *reinterpret_cast<const uint32_t*>(in + c0 / 2);
-            else w[k] = *reinterpret_cast<const uint2*>(in + c0);
-        } else if (fmt == kQE2m1) {
-            for (int j = 0; j < 4; ++j)
-                if (c0 / 2 + j < p.code_bytes) w[k].x |= (uint32_t)in[c0 / 2 + j] << (8 * j);
+        if constexpr (W == 8) {
+            const long long o = kFlat ? u * 8 : c0;
+            if (fmt == kQE2m1) w[k].x = *reinterpret_cast<const uint32_t*>((kFlat ? codes : in) + o / 2);
+            else w[k] = *reinterpret_cast<const uint2*>((kFlat ? codes : in) + o);
         } else {
-            for (int j = 0; j < 8; ++j)
-                if (c0 + j < p.C) (j < 4 ? w[k].x : w[k].y) |= (uint32_t)in[c0 + j] << (8 * (j & 3));
+            w[k] = get_codes<W>(in + (fmt == kQE2m1 ? c0 / 2 : c0), p.C - c0, fmt == kQE2m1);
         }
     }
 #pragma unroll
@@ -240,8 +343,10 @@ __global__ void __launch_bounds__(kQThreads) qcache_read_kernel(const __grid_con
         float x[8];
         decode8(w[k], c[k], fmt, x);
         T* row = kFlat ? dst + (u0 + k * kQThreads) * 8 : dst + at[k].px * p.C;
-        if (in_bounds(&g_block_status, row, (kFlat ? 8 : p.C) * (long long)sizeof(T), p.dst, o_bytes))
-            store8<T, V>(pack8<T, V>(x), row, at[k].r * 8, 1, kFlat ? 8 : p.C);
+        if (!in_bounds(&g_block_status, row, (kFlat ? 8 : p.C) * (long long)sizeof(T), p.dst, o_bytes))
+            continue;
+        if constexpr (W == 8) store8<T, true>(pack8<T, true>(x), row, at[k].r * 8, 1, kFlat ? 8 : p.C);
+        else store_w<T, W>(x, row + at[k].r * 8, p.C - at[k].r * 8);
     }
 }
 

@@ -73,7 +73,8 @@ def _values(shape, dtype, seed):
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("N,H,W,C,slots", [
     (1, 9, 11, 96, 3), (2, 5, 7, 16, 4), (1, 3, 5, 33, 3), (1, 13, 1, 1, 2), (2, 4, 6, 100, 5),
-    (1, 6, 5, 40, 3), (1, 2, 3, 1055, 3), (1, 1, 1, 2048, 1), (1, 8, 9, 64, 2), (3, 4, 4, 31, 4)])
+    (1, 6, 5, 40, 3), (1, 2, 3, 1055, 3), (1, 1, 1, 2048, 1), (1, 8, 9, 64, 2), (3, 4, 4, 31, 4),
+    (1, 7, 5, 68, 3), (2, 5, 3, 12, 3), (1, 9, 4, 202, 2), (1, 33, 40, 6, 2)])
 def test_write_and_read_exact(N, H, W, C, slots, dtype, fmt):
     desc = ccv3d.make_qcache_desc(N=N, H=H, W=W, C=C, ring_slots=slots, format=fmt, dtype=dtype)
     cb, sb = ccv3d.ccv3d_qcache_sizes(desc)
