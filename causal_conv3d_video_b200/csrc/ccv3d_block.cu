@@ -143,10 +143,29 @@ void allow_smem() {
     done[dev].store(true, std::memory_order_release);
 }
 
+// Blocks of K with that many threads (a multiple of 32, at most 512) that an SM
+// holds at once: a grid that walks its rows takes exactly as many, since a part
+// of a second wave would cost a whole one.
+template <auto* K>
+int blocks_an_sm(int threads) {
+    static std::atomic<int> known[17];
+    std::atomic<int>& k = known[threads / 32];
+    int n = k.load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, K, threads, 0) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = 1;
+        }
+        k.store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 template <typename T, bool V, bool B, int TPR, int NU>
 void norm_fwd_run(const NormFwd& p, const RowShape& r, cudaStream_t st) {
     if constexpr (TPR == 0) {
-        const int grid = (int)std::min<long long>(p.rows, (long long)kSms * std::max(1, 1024 / r.threads));
+        const int grid = (int)std::min<long long>(
+            p.rows, (long long)kSms * blocks_an_sm<norm_fwd_rows<T, V, NU, B>>(r.threads));
         norm_fwd_rows<T, V, NU, B><<<grid, r.threads, 0, st>>>(p);
     } else {
         const TileLaunch l = tile_launch(r, p.C, sizeof(T), p.rows, B ? 2 : 1, 4, 20 * 1024, 768);

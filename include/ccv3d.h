@@ -337,7 +337,7 @@ typedef struct {
     int C;                /* channels, 1 .. CCV3D_NORM_MAX_C */
     ccv3d_norm_kind pre;  /* NONE: no y */
     ccv3d_norm_kind post; /* NONE: b is added as it is */
-    ccv3d_act act;
+    ccv3d_act act;        /* after the pre norm; ignored without it */
     float eps;            /* > 0, finite */
     float scale;          /* residual scale, finite */
     long long gate_rows;  /* consecutive rows that share a row of the gate (all
