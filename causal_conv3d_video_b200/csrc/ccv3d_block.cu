@@ -76,7 +76,7 @@ bool gate_fits(const ccv3d_norm_desc* d, const void* gate) {
 // Threads that share a row (0: the block's) and eight-channel units a thread.
 // Within a warp the least idle of the shapes the kernels are built for (the
 // decoder's widths, three times a power of two, leave no thread idle), of
-// equals the one with the most threads a row; single-channel loads (C not a
+// equals the one with the fewest threads a row (the fewest shuffles); single-channel loads (C not a
 // multiple of 8) want 16 threads side by side.  Wider rows take a block each.
 struct RowShape {
     int tpr, units, threads;
@@ -88,7 +88,7 @@ RowShape row_shape(int C, bool vec, int max_units) {
     int cover = 1 << 30;
     for (int u = 1; u <= max_units; ++u)
         for (int tpr = vec ? 4 : 16; tpr <= 32; tpr *= 2)
-            if (tpr * u >= n && tpr * u < cover) {
+            if (tpr * u >= n && tpr * u <= cover) {
                 cover = tpr * u;
                 best = {tpr, u, 0};
             }
@@ -175,9 +175,9 @@ void norm_fwd_run(const NormFwd& p, const RowShape& r, cudaStream_t st) {
     }
 }
 
-// Units a thread at most, backward: the general form's four column sums leave
-// registers for two.
-constexpr int bwd_units(bool gen) { return gen ? 2 : 3; }
+// Units a thread at most, backward: the four column sums of a call with biases
+// leave registers for two.
+constexpr int bwd_units(int form) { return form == kBwdBiased ? 2 : 3; }
 
 // Launch shape of the backward pass: blocks per gate group.
 struct BwdShape {
@@ -185,10 +185,13 @@ struct BwdShape {
     TileLaunch tile;
     long long groups, group_rows;
     int blocks_per_group;
+    int sums;  // column sums the kernel takes: 2 or 4
 };
-BwdShape bwd_shape(const ccv3d_norm_desc* d, bool gated, bool gen) {
+BwdShape bwd_shape(const ccv3d_norm_desc* d, bool gated, int form) {
     BwdShape b = {};
-    b.row = row_shape(d->C, d->C % 8 == 0, bwd_units(gen));
+    // (the wide-row kernel has one form for means and biases)
+    b.row = row_shape(d->C, d->C % 8 == 0, bwd_units(form));
+    b.sums = form == kBwdBiased || (form != kBwdRms && b.row.tpr == 0) ? 4 : 2;
     b.groups = gated ? d->rows / d->gate_rows : 1;
     b.group_rows = gated ? d->gate_rows : d->rows;
     long long steps = b.group_rows, blocks;
@@ -203,14 +206,14 @@ BwdShape bwd_shape(const ccv3d_norm_desc* d, bool gated, bool gen) {
     return b;
 }
 
-template <typename T, bool V, bool B, int TPR, int NU>
+template <typename T, bool V, int F, int TPR, int NU>
 void norm_bwd_run(const NormBwd& p, const BwdShape& s, cudaStream_t st) {
     const int grid = (int)(s.groups * s.blocks_per_group);
     if constexpr (TPR == 0) {
-        norm_bwd_rows<T, V, NU, B><<<grid, s.row.threads, 0, st>>>(p);
+        norm_bwd_rows<T, V, NU, F != kBwdRms><<<grid, s.row.threads, 0, st>>>(p);
     } else {
-        allow_smem<norm_bwd_tiles<T, V, TPR, NU, B>>();
-        norm_bwd_tiles<T, V, TPR, NU, B><<<grid, s.tile.threads, s.tile.smem, st>>>(p, s.tile.t);
+        allow_smem<norm_bwd_tiles<T, V, TPR, NU, F>>();
+        norm_bwd_tiles<T, V, TPR, NU, F><<<grid, s.tile.threads, s.tile.smem, st>>>(p, s.tile.t);
     }
 }
 
@@ -238,9 +241,11 @@ void norm_fwd_shape(const NormFwd& p, cudaStream_t st) {
     const RowShape r = row_shape(p.C, V, p.rows < 2 * kSms ? 0 : 3);
     with_shape<V, 3>(r, [&](auto tpr, auto nu) { norm_fwd_run<T, V, B, tpr(), nu()>(p, r, st); });
 }
-template <typename T, bool V, bool B>
+template <typename T, bool V, int F>
 void norm_bwd_shape(const NormBwd& p, const BwdShape& s, cudaStream_t st) {
-    with_shape<V, bwd_units(B)>(s.row, [&](auto tpr, auto nu) { norm_bwd_run<T, V, B, tpr(), nu()>(p, s, st); });
+    with_shape<V, bwd_units(F)>(s.row, [&](auto tpr, auto nu) {
+        norm_bwd_run<T, V, F, tpr(), nu()>(p, s, st);
+    });
 }
 
 template <typename T>
@@ -251,12 +256,16 @@ void norm_fwd_type(const NormFwd& p, cudaStream_t st) {
         p.b != nullptr ? norm_fwd_shape<T, false, true>(p, st)
                        : norm_fwd_shape<T, false, false>(p, st);
 }
+template <typename T, bool V>
+void norm_bwd_form(const NormBwd& p, const BwdShape& s, int form, cudaStream_t st) {
+    if (form == kBwdRms) norm_bwd_shape<T, V, kBwdRms>(p, s, st);
+    else if (form == kBwdMeans) norm_bwd_shape<T, V, kBwdMeans>(p, s, st);
+    else norm_bwd_shape<T, V, kBwdBiased>(p, s, st);
+}
 template <typename T>
-void norm_bwd_type(const NormBwd& p, const BwdShape& s, bool gen, cudaStream_t st) {
-    if (p.C % 8 == 0)
-        gen ? norm_bwd_shape<T, true, true>(p, s, st) : norm_bwd_shape<T, true, false>(p, s, st);
-    else
-        gen ? norm_bwd_shape<T, false, true>(p, s, st) : norm_bwd_shape<T, false, false>(p, s, st);
+void norm_bwd_type(const NormBwd& p, const BwdShape& s, int form, cudaStream_t st) {
+    if (p.C % 8 == 0) norm_bwd_form<T, true>(p, s, form, st);
+    else norm_bwd_form<T, false>(p, s, form, st);
 }
 
 // --------------------------------------------------------------- pointwise
@@ -803,11 +812,11 @@ size_t ccv3d_norm_workspace(const ccv3d_norm_desc* d) {
     if (check_norm(d) != CCV3D_OK || d->rows == 0) return 0;
     // with a gate or without one, with biases or without: the largest of them
     long long slots = 0;
-    for (int form = 0; form < 4; ++form) {
-        const bool gated = form & 1, gen = form & 2;
+    for (int call = 0; call < 6; ++call) {
+        const bool gated = call & 1;
         if (gated && (d->gate_rows < 1 || d->rows % d->gate_rows != 0)) continue;
-        const BwdShape b = bwd_shape(d, gated, gen);
-        slots = std::max(slots, b.groups * b.blocks_per_group * (gen ? 4 : 2));
+        const BwdShape b = bwd_shape(d, gated, call / 2);
+        slots = std::max(slots, b.groups * b.blocks_per_group * b.sums);
     }
     return (size_t)slots * d->C * sizeof(float);
 }
@@ -857,24 +866,24 @@ ccv3d_status ccv3d_norm_backward(const ccv3d_norm_desc* d, const void* h_out, co
     bufs.out(ws, need);
     const ccv3d_status k = bufs.check();
     if (k != CCV3D_OK) return k;
-    // the general form: biases, whose gradients (and dgate, to which post_bias adds) are
-    // sums of du and G, or layer norms
-    const bool bias = pre_bias != nullptr || post_bias != nullptr ||
-                      d->pre == CCV3D_NORM_LAYER || d->post == CCV3D_NORM_LAYER;
-    const BwdShape s = bwd_shape(d, gate != nullptr, bias);
+    // bias gradients, and dgate, to which post_bias adds, want the sums of du and G
+    const int form = pre_bias != nullptr || post_bias != nullptr ? kBwdBiased
+                     : d->pre == CCV3D_NORM_LAYER || d->post == CCV3D_NORM_LAYER ? kBwdMeans
+                                                                                 : kBwdRms;
+    const BwdShape s = bwd_shape(d, gate != nullptr, form);
     const long long slots = s.groups * s.blocks_per_group;
     if (slots > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;
     const NormBwd p = {h_out, b, gate, post_w, post_bias, pre_w, pre_bias, dy, dh_out, dh, db,
                        sums ? static_cast<float*>(ws) : nullptr, d->rows, s.group_rows, s.groups,
                        slots, s.blocks_per_group, d->C, d->pre, d->post, d->act, d->eps, d->scale,
                        1.0f / (float)d->C};
-    if (d->dtype == CCV3D_BF16) norm_bwd_type<bf16>(p, s, bias, stream);
-    else norm_bwd_type<float>(p, s, bias, stream);
+    if (d->dtype == CCV3D_BF16) norm_bwd_type<bf16>(p, s, form, stream);
+    else norm_bwd_type<float>(p, s, form, stream);
     if (launched() != CCV3D_OK) return CCV3D_ERR_CUDA;
     if (!sums) return CCV3D_OK;
     float* part = static_cast<float*>(ws);
     const NormFin f = {part, part, gate, post_w, post_bias, dgate, dpost_w, dpost_bias, dpre_w,
-                       dpre_bias, s.groups, slots, s.blocks_per_group, d->C, bias ? 1 : 0,
+                       dpre_bias, s.groups, slots, s.blocks_per_group, d->C, s.sums == 4 ? 1 : 0,
                        b != nullptr ? 1 : 0, d->scale};
     const dim3 grid((unsigned)up(d->C, kFinCols), (unsigned)std::min<long long>(s.groups, 32768));
     const dim3 block(kFinCols, kFinRows);

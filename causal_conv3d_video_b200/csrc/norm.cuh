@@ -721,11 +721,16 @@ __global__ void __launch_bounds__(kTileThreads, 3) norm_fwd_tiles(
     }
 }
 
-template <typename T, bool V, int TPR, int NU, bool kGen>
+// kForm: kBwdRms, RMS norms without biases (two column sums, no row means);
+// kBwdMeans, a layer norm is there; kBwdBiased, a bias is (four column sums:
+// du and G too).
+constexpr int kBwdRms = 0, kBwdMeans = 1, kBwdBiased = 2;
+template <typename T, bool V, int TPR, int NU, int kForm>
 __global__ void __launch_bounds__(kTileThreads, 2) norm_bwd_tiles(
     const __grid_constant__ NormBwd p, const __grid_constant__ TileShape sh) {
     extern __shared__ __align__(128) uint8_t tile_smem[];
-    constexpr int nT = 4, kQ = kGen ? 4 : 2;
+    constexpr int nT = 4, kQ = kForm == kBwdBiased ? 4 : 2;
+    constexpr bool kMean = kForm != kBwdRms, kBias = kForm == kBwdBiased;
     const int rpp = (int)blockDim.x / TPR;  // rows a pass
     const int lane = (int)threadIdx.x % TPR, sub = (int)threadIdx.x / TPR, C = p.C;
     const int row_bytes = C * (int)sizeof(T);
@@ -791,7 +796,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_bwd_tiles(
                     tile_unit<T, V, TPR>(v[u], in, u, lane, C, ok);
                     tile_unit<T, V, TPR>(G[u], in + sh.cap, u, lane, C, ok);
                 }
-                const float rstd = normalise2<V, TPR, NU>(v, kGen ? p.pre : kNormRms, lane, C,
+                const float rstd = normalise2<V, TPR, NU>(v, kMean ? p.pre : kNormRms, lane, C,
                                                           p.eps, p.inv_c);
                 f2 s0 = f2_all(0.0f), s1 = f2_all(0.0f);
 #pragma unroll
@@ -799,11 +804,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_bwd_tiles(
                     const int c0 = unit_c0<V>(u, lane, TPR);
                     f2 w[4], wb[4];
                     vec8(w, vecs, V, c0, TPR);
-                    if constexpr (kGen) vec8(wb, vecs + L, V, c0, TPR);
+                    if constexpr (kBias) vec8(wb, vecs + L, V, c0, TPR);
                     auto slope = [&](int kind) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const f2 a = kGen ? f2_fma(v[u][i], w[i], wb[i]) : f2_mul(v[u][i], w[i]);
+                            const f2 a = kBias ? f2_fma(v[u][i], w[i], wb[i]) : f2_mul(v[u][i], w[i]);
                             G[u][i] = f2_mul(G[u][i], f2_act_grad<T>(a, kind));
                         }
                     };
@@ -812,27 +817,27 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_bwd_tiles(
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         acc[0][u][i] = f2_fma(G[u][i], v[u][i], acc[0][u][i]);
-                        if constexpr (kGen) acc[2][u][i] = f2_add(acc[2][u][i], G[u][i]);
+                        if constexpr (kBias) acc[2][u][i] = f2_add(acc[2][u][i], G[u][i]);
                         G[u][i] = f2_mul(G[u][i], w[i]);
                         s0 = f2_fma(G[u][i], v[u][i], s0);
-                        if constexpr (kGen) s1 = f2_add(s1, G[u][i]);
+                        if constexpr (kMean) s1 = f2_add(s1, G[u][i]);
                     }
                 }
-                float s[kGen ? 2 : 1];
+                float s[kMean ? 2 : 1];
                 s[0] = f2_sum(s0);
-                if constexpr (kGen) s[1] = f2_sum(s1);
+                if constexpr (kMean) s[1] = f2_sum(s1);
                 int turn = 0;
-                row_sum<TPR, kGen ? 2 : 1>(s, nullptr, turn);
+                row_sum<TPR, kMean ? 2 : 1>(s, nullptr, turn);
                 const f2 a = f2_all(-s[0] * p.inv_c), r2 = f2_all(rstd);
                 f2 mean = f2_all(0.0f);
-                if constexpr (kGen) mean = f2_all(p.pre == kNormLayer ? -s[1] * p.inv_c : 0.0f);
+                if constexpr (kMean) mean = f2_all(p.pre == kNormLayer ? -s[1] * p.inv_c : 0.0f);
 #pragma unroll
                 for (int u = 0; u < NU; ++u) {
                     f2 g[4];
                     tile_unit<T, V, TPR>(g, in + 2 * sh.cap, u, lane, C, ok && p.dh_out != nullptr);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        G[u][i] = f2_fma(r2, f2_fma(v[u][i], a, kGen ? f2_add(G[u][i], mean) : G[u][i]),
+                        G[u][i] = f2_fma(r2, f2_fma(v[u][i], a, kMean ? f2_add(G[u][i], mean) : G[u][i]),
                                          g[i]);
                 }
             } else {
@@ -851,7 +856,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_bwd_tiles(
                     tile_unit<T, V, TPR>(v[u], in + 3 * sh.cap, u, lane, C, ok);
                 float rstd = 1.0f;
                 if (p.post != kNormNone)
-                    rstd = normalise2<V, TPR, NU>(v, kGen ? p.post : kNormRms, lane, C, p.eps,
+                    rstd = normalise2<V, TPR, NU>(v, kMean ? p.post : kNormRms, lane, C, p.eps,
                                                   p.inv_c);
                 f2 s0 = f2_all(0.0f), s1 = f2_all(0.0f);
 #pragma unroll
@@ -863,28 +868,28 @@ __global__ void __launch_bounds__(kTileThreads, 2) norm_bwd_tiles(
                         acc[1][u][i] = f2_fma(G[u][i], v[u][i], acc[1][u][i]);
                         // (past C, G may hold a row's mean: v and g are 0 there, and the
                         // sums of those columns are not written)
-                        if constexpr (kGen) acc[3][u][i] = f2_add(acc[3][u][i], G[u][i]);
+                        if constexpr (kBias) acc[3][u][i] = f2_add(acc[3][u][i], G[u][i]);
                         G[u][i] = f2_mul(G[u][i], g[i]);
                         s0 = f2_fma(G[u][i], v[u][i], s0);
-                        if constexpr (kGen) s1 = f2_add(s1, G[u][i]);
+                        if constexpr (kMean) s1 = f2_add(s1, G[u][i]);
                     }
                 }
                 if (p.db != nullptr) {
                     if (p.post != kNormNone) {
-                        float s[kGen ? 2 : 1];
+                        float s[kMean ? 2 : 1];
                         s[0] = f2_sum(s0);
-                        if constexpr (kGen) s[1] = f2_sum(s1);
+                        if constexpr (kMean) s[1] = f2_sum(s1);
                         int turn = 0;
-                        row_sum<TPR, kGen ? 2 : 1>(s, nullptr, turn);
+                        row_sum<TPR, kMean ? 2 : 1>(s, nullptr, turn);
                         const f2 a = f2_all(-s[0] * p.inv_c), r2 = f2_all(rstd);
                         f2 mean = f2_all(0.0f);
-                        if constexpr (kGen) mean = f2_all(p.post == kNormLayer ? -s[1] * p.inv_c : 0.0f);
+                        if constexpr (kMean) mean = f2_all(p.post == kNormLayer ? -s[1] * p.inv_c : 0.0f);
 #pragma unroll
                         for (int u = 0; u < NU; ++u)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 G[u][i] = f2_mul(r2, f2_fma(v[u][i], a,
-                                                            kGen ? f2_add(G[u][i], mean) : G[u][i]));
+                                                            kMean ? f2_add(G[u][i], mean) : G[u][i]));
                     }
                     if (ok)
 #pragma unroll
