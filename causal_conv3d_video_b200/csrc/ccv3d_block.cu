@@ -175,10 +175,6 @@ void norm_fwd_run(const NormFwd& p, const RowShape& r, cudaStream_t st) {
     }
 }
 
-// Units a thread at most, backward: the four column sums of a call with biases
-// leave registers for two.
-constexpr int bwd_units(int form) { return form == kBwdBiased ? 2 : 3; }
-
 // Launch shape of the backward pass: blocks per gate group.
 struct BwdShape {
     RowShape row;
@@ -190,7 +186,7 @@ struct BwdShape {
 BwdShape bwd_shape(const ccv3d_norm_desc* d, bool gated, int form) {
     BwdShape b = {};
     // (the wide-row kernel has one form for means and biases)
-    b.row = row_shape(d->C, d->C % 8 == 0, bwd_units(form));
+    b.row = row_shape(d->C, d->C % 8 == 0, 3);
     b.sums = form == kBwdBiased || (form != kBwdRms && b.row.tpr == 0) ? 4 : 2;
     b.groups = gated ? d->rows / d->gate_rows : 1;
     b.group_rows = gated ? d->gate_rows : d->rows;
@@ -198,7 +194,8 @@ BwdShape bwd_shape(const ccv3d_norm_desc* d, bool gated, int form) {
     if (b.row.tpr == 0) {
         blocks = (long long)kSms * std::max(1, 512 / b.row.threads);
     } else {
-        b.tile = tile_launch(b.row, d->C, (int)size_of(d->dtype), b.group_rows, 4, 3, 52 * 1024, 512);
+        b.tile = tile_launch(b.row, d->C, (int)size_of(d->dtype), b.group_rows, 4, 3, 52 * 1024,
+                             bwd_blocks(form, b.row.units) * kTileThreads);
         blocks = kSms * b.tile.blocks_per_sm;
         steps = up(b.group_rows, b.tile.t.rows);
     }
@@ -218,12 +215,12 @@ void norm_bwd_run(const NormBwd& p, const BwdShape& s, cudaStream_t st) {
 }
 
 // Calls f with the constants (TPR, units) of a shape.
-template <bool V, int U, typename F>
+template <bool V, typename F>
 void with_shape(const RowShape& r, F&& f) {
     auto units = [&](auto tpr) {
         if (r.units == 1) f(tpr, std::integral_constant<int, 1>());
         else if (r.units == 2) f(tpr, std::integral_constant<int, 2>());
-        else if constexpr (U > 2 && decltype(tpr)::value != 0) f(tpr, std::integral_constant<int, 3>());
+        else if constexpr (decltype(tpr)::value != 0) f(tpr, std::integral_constant<int, 3>());
     };
     switch (r.tpr) {
         case 4: if constexpr (V) units(std::integral_constant<int, 4>()); break;
@@ -239,11 +236,11 @@ void norm_fwd_shape(const NormFwd& p, cudaStream_t st) {
     // few rows (under two an SM): a block each, without the ring's start-up
     // (one row of 768: 3.3 us against 5.7)
     const RowShape r = row_shape(p.C, V, p.rows < 2 * kSms ? 0 : 3);
-    with_shape<V, 3>(r, [&](auto tpr, auto nu) { norm_fwd_run<T, V, B, tpr(), nu()>(p, r, st); });
+    with_shape<V>(r, [&](auto tpr, auto nu) { norm_fwd_run<T, V, B, tpr(), nu()>(p, r, st); });
 }
 template <typename T, bool V, int F>
 void norm_bwd_shape(const NormBwd& p, const BwdShape& s, cudaStream_t st) {
-    with_shape<V, bwd_units(F)>(s.row, [&](auto tpr, auto nu) {
+    with_shape<V>(s.row, [&](auto tpr, auto nu) {
         norm_bwd_run<T, V, F, tpr(), nu()>(p, s, st);
     });
 }

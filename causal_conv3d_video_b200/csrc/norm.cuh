@@ -725,8 +725,14 @@ __global__ void __launch_bounds__(kTileThreads, 3) norm_fwd_tiles(
 // kBwdMeans, a layer norm is there; kBwdBiased, a bias is (four column sums:
 // du and G too).
 constexpr int kBwdRms = 0, kBwdMeans = 1, kBwdBiased = 2;
+// 256-thread blocks an SM: four column sums of two or three units take more than
+// 128 registers a thread (spilled at two blocks: 398 us against 230 for 900000 x
+// 96, two layer norms with biases).
+__host__ __device__ constexpr int bwd_blocks(int form, int units) {
+    return form == kBwdBiased && units > 1 ? 1 : 2;
+}
 template <typename T, bool V, int TPR, int NU, int kForm>
-__global__ void __launch_bounds__(kTileThreads, 2) norm_bwd_tiles(
+__global__ void __launch_bounds__(kTileThreads, bwd_blocks(kForm, NU)) norm_bwd_tiles(
     const __grid_constant__ NormBwd p, const __grid_constant__ TileShape sh) {
     extern __shared__ __align__(128) uint8_t tile_smem[];
     constexpr int nT = 4, kQ = kForm == kBwdBiased ? 4 : 2;
