@@ -278,30 +278,38 @@ ccv3d_status check_pointwise(const ccv3d_pointwise_desc* d) {
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Shape of a product on FFMA: tiles of 128 x 128, or of 64 x 64 or 128 x 32
-// where less of them is lost at the edges or in the last wave (their values
-// count 1.5 times a 128 x 128 tile's: half the FMAs per shared-memory read), and
-// splits of the reduction while that leaves SMs without a block, of at least 8
-// steps of 16.
+// Shape of a product on FFMA: the tile (128 x 128, 64 x 64, 128 x 32 or 32 x 128)
+// and the splits of the reduction with the shortest time on the fullest SM
+// (blocks on one SM share its time), in FMAs at about 83 a cycle and SM for the
+// largest tile; the others' count 1.5 times (half the FMAs per shared-memory
+// read).  Splits are of at least 8 steps of 16; joining them is a launch and two
+// trips of the partials.  A sum of more than 4096 terms (dw over many pixels)
+// is split for its accuracy too, as far as 256 MB of partials allow: one chain
+// of 12318 fp32 FMAs is 1.1e-6 off (2-norm), chains of 4096 half of that.
 struct SimtShape {
     int tm, tn, splits;
     long long tiles, k_per_split;
 };
 SimtShape simt_shape(long long M, long long N, long long K) {
-    constexpr int kTiles[3][2] = {{128, 128}, {64, 64}, {128, 32}};
+    constexpr int kTiles[4][2] = {{128, 128}, {64, 64}, {128, 32}, {32, 128}};
     SimtShape best = {};
     double cost = 1e300;
+    const long long fit = std::max<long long>(1, std::min<long long>((256LL << 20) / (M * N * 4), 16384));
+    const long long least = std::min(up(K, 4096), fit);
     for (const auto& t : kTiles) {
         const long long tiles = up(M, t[0]) * up(N, t[1]);
-        const int want = (int)std::max<long long>(1, std::min<long long>({2 * kSms / tiles, up(K, 128), 512}));
-        const long long per = up(up(K, want), kPwK) * kPwK;
-        const int splits = (int)std::max<long long>(1, up(K, per));
-        // (blocks on one SM share its time: what counts is the fullest SM's share)
-        const double c = std::ceil((double)tiles * splits / kSms) * (double)t[0] * t[1] * (per + 32) *
-                         (t[1] == 128 ? 1.0 : 1.5);
-        if (c < cost) {
-            cost = c;
-            best = {t[0], t[1], splits, tiles, per};
+        for (const int more : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 64, 128}) {
+            const long long want = least * more;
+            if (more > 1 && (want > up(K, 128) || want > 512 || tiles * want > 8 * kSms)) break;
+            const long long per = up(up(K, want), kPwK) * kPwK;
+            const int splits = (int)std::max<long long>(1, up(K, per));
+            double c = std::ceil((double)tiles * splits / kSms) * (double)t[0] * t[1] * (per + 32) *
+                       (t[0] == 128 && t[1] == 128 ? 1.0 : 1.5);
+            if (splits > 1) c += 83.0 * (4000.0 + (double)splits * M * N * 8.0 / 3500.0);
+            if (c < cost) {
+                cost = c;
+                best = {t[0], t[1], splits, tiles, per};
+            }
         }
     }
     return best;
@@ -610,7 +618,8 @@ ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb
     p.o.partial = p.splits > 1 ? partial : nullptr;
     if (s.tiles > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)s.tiles, 1, p.splits);
-    if (s.tn == 128) pw_simt_kernel<float, AK, BK, 128, 128><<<grid, 256, 0, st>>>(p);
+    if (s.tm == 32) pw_simt_kernel<float, AK, BK, 32, 128><<<grid, 256, 0, st>>>(p);
+    else if (s.tn == 128) pw_simt_kernel<float, AK, BK, 128, 128><<<grid, 256, 0, st>>>(p);
     else if (s.tn == 64) pw_simt_kernel<float, AK, BK, 64, 64><<<grid, 256, 0, st>>>(p);
     else pw_simt_kernel<float, AK, BK, 128, 32><<<grid, 256, 0, st>>>(p);
     if (p.splits > 1) {

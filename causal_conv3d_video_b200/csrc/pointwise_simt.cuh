@@ -115,7 +115,7 @@ struct PwFetch {
     }
 };
 
-// SM x SN tile a block (128 x 128, 64 x 64 or 128 x 32), k in steps of 16
+// SM x SN tile a block (128 x 128, 64 x 64, 128 x 32 or 32 x 128), k in steps of 16
 // through two shared-memory buffers; the next step's operands wait in
 // registers.  A thread has 4 rows by 4 columns of each SM/GM x SN/GN part.  The
 // largest has the best ratio of FMAs to shared-memory reads, the others are for
@@ -123,7 +123,7 @@ struct PwFetch {
 template <typename T, bool AK, bool BK, int SM, int SN>
 __global__ void __launch_bounds__(256, SM * SN == 128 * 128 ? 2 : 4) pw_simt_kernel(
     const __grid_constant__ PwSimt p) {
-    constexpr int kTx = SN >= 64 ? 16 : 8, kTy = 256 / kTx;  // threads across and down
+    constexpr int kTx = SN == 32 ? 8 : (SM == 32 ? 32 : 16), kTy = 256 / kTx;  // threads across, down
     constexpr int kHm = SM / (kTy * 4), kHn = SN / (kTx * 4);
     constexpr int kA = 2 * kPwK * (SM + kPwPad), kB = 2 * kPwK * (SN + kPwPad);
     typedef float SlabA[2][kPwK][SM + kPwPad];
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(256, SM * SN == 128 * 128 ? 2 : 4) pw_simt_ker
 #pragma unroll
         for (int j = 0; j < kHn * 2; ++j) acc[i][j] = f2_all(0.0f);
     float va[SM / 16], vb[SN / 16];
-    PwFetch<T, AK, SM> fa(A, p.a_elems, p.sam, p.sak, m0, p.M, kb, tid, p.vec);
+    PwFetch<T, AK, SM> fa(A, p.a_elems, p.sam, p.sak, m0, p.M, kb, tid, p.vec && SM >= 64);
     PwFetch<T, BK, SN> fb(B, p.b_elems, p.sbn, p.sbk, n0, p.N, kb, tid, p.vec && SN >= 64);
     int left = (int)(ke - kb);
     fa(va, left);

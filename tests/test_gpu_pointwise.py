@@ -180,6 +180,17 @@ def test_backward_many_tiles():
     _check_backward(_case(100_003, 40, 24, "bf16"))
 
 
+def test_fp32_long_sums_keep_their_accuracy():
+    """dw over 60000 pixels in fp32: chains of at most 4096 FMAs.  Rounding errors of
+    a chain add up like a random walk whose steps are 2^-24 of the running sum: in
+    the 2-norm about 2^-24 sqrt(4096 / 2) / sqrt(3) = 1.6e-6 of a chain's share if
+    every step were at its bound, a third of that for steps uniform within it."""
+    s = _case(60_000, 40, 72, "fp32")
+    _, dout, got = _backward(s)
+    for k, want in (("dw", d(dout).t() @ d(s["x"])), ("dbias", d(dout).sum(0))):
+        assert (d(got[k]) - want).norm() <= 1.0e-6 * want.norm(), k
+
+
 def test_gradients_against_differences():
     """fp32: central differences of the 64-bit definition along random directions."""
     s = _case(40, 24, 36, "fp32", actk="gelu", bias=True)
