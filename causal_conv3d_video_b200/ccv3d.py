@@ -8,6 +8,7 @@ the import of this module fails loudly: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -611,6 +612,12 @@ class Plan:
 
     def forward_qring(self, x, desc, codes, scales, head, cache_buf, w, bias, out, stream=None):
         """Call with its ring cache in 8 or 4 bits; returns the head of the new cache."""
+        d, frame = self.desc, self.desc.N * self.desc.H * self.desc.W * self.desc.Cin
+        for name, t, n in (("x", x, frame * d.T_x), ("cache_buf", cache_buf, frame * d.cache_len),
+                           ("w", w, d.Cout * d.kt * d.kh * d.kw * d.Cin), ("bias", bias, d.Cout),
+                           ("out", out, math.prod(self.out_shape()))):
+            if t is not None and not isinstance(t, int) and t.numel() != n:
+                raise ValueError(f"forward_qring: {name} has {t.numel()} elements, not {n}")
         return ccv3d_forward_qring(self.handle, x, desc, codes, scales, head, cache_buf, w, bias,
                                    out, self.stride, self.pad, self.dilation, stream)[1]
 

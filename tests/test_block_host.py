@@ -248,5 +248,18 @@ def test_binding_refuses_wrong_tensors():
             ccv3d.ccv3d_norm_forward(desc, h, None, None, None, None, None, None, None, A, stream=0)
 
 
+def test_plan_forward_qring_checks_sizes():
+    import torch
+    plan = ccv3d.Plan(ccv3d.make_desc(N=1, Cin=96, Cout=32, H=4, W=6, T_x=1, cache_len=2))
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    good = dict(x=bf(1, 1, 4, 6, 96), cache_buf=bf(1, 2, 4, 6, 96), w=bf(32, 3, 3, 3, 96),
+                bias=bf(32), out=bf(1, 1, 4, 6, 32))
+    for name in good:
+        a = dict(good, **{name: bf(*good[name].shape)[..., :-8].contiguous()})
+        with pytest.raises(ValueError, match=name):
+            plan.forward_qring(a["x"], qdesc(), _addr(1), _addr(2), 0, a["cache_buf"], a["w"],
+                               a["bias"], a["out"], stream=0)
+
+
 def test_strerror_names_every_status():
     assert all(ccv3d.ccv3d_strerror(s) != "unknown status" for s in range(10))
