@@ -2,8 +2,9 @@
 
     python -m causal_conv3d_video_b200.build [--force] [--verbose-ptxas]
 
-The library is two translation units (csrc/ccv3d.cu: the convolution,
-csrc/ccv3d_block.cu: the operators around it) exporting the C ABI declared in
+The library is four translation units (csrc/ccv3d.cu: the convolution,
+csrc/ccv3d_block.cu: the operators around it, csrc/norm_bf16.cu and
+csrc/norm_fp32.cu: the norms' kernels) exporting the C ABI declared in
 include/ccv3d.h.  The CUDA runtime is linked statically; the
 driver's cuTensorMapEncodeTiled is reached through cudaGetDriverEntryPoint,
 so no -lcuda is needed at link time.
@@ -25,6 +26,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libccv3d.so")
 # the bounds-checked build (-DCCV3D_CHECKED): every computed global address is
 # range-checked before use; a violation is reported as CCV3D_ERR_BOUNDS
 CHECKED_LIB_PATH = os.path.join(LIB_DIR, "libccv3d_checked.so")
+UNITS = ("ccv3d.cu", "ccv3d_block.cu", "norm_bf16.cu", "norm_fp32.cu")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -56,8 +58,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, checked: bool = Fals
     cmd = [_nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared",
            "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
            "-I", os.path.join(ROOT, "include"),
-           "--threads", "2", os.path.join(CSRC, "ccv3d.cu"),
-           os.path.join(CSRC, "ccv3d_block.cu"), "-o", tmp]
+           "--threads", str(len(UNITS)), *(os.path.join(CSRC, u) for u in UNITS), "-o", tmp]
     if checked:
         cmd[1:1] = ["-DCCV3D_CHECKED"]
     if verbose_ptxas:

@@ -12,9 +12,10 @@ namespace ccv3d {
 
 typedef __nv_bfloat16 bf16_t;
 
-// First error recorded on this device by a kernel of ccv3d_norm_*,
-// ccv3d_pointwise_* or ccv3d_qcache_* (0: none): a bounded wait that ran out,
-// or a bounds violation of the checked build.
+// First error recorded on this device by a kernel of this translation unit (0:
+// none): a bounded wait that ran out, or a bounds violation of the checked build.
+// ccv3d_block_get_status reads that of each of ccv3d_norm_*, ccv3d_pointwise_* and
+// ccv3d_qcache_*.
 static __device__ int g_block_status;
 
 enum ActKind { kActNone = 0, kActSilu = 1, kActGelu = 2 };

@@ -160,3 +160,96 @@ def status_is_clean():
     """No call of a test left an error in the library's status word."""
     yield
     assert ccv3d.ccv3d_block_get_status() == ccv3d.CCV3D_OK
+
+
+def test_two_streams_at_once():
+    """The operators on two streams, each with its own workspaces, overlapping on
+    the GPU: the bits of the same calls one after the other."""
+    def job(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda *s: torch.randn(s, device="cuda", generator=g).bfloat16()
+        M, C, K = 6000, 96, 192
+        x, w, res, dout = rnd(M, K), rnd(C, K), rnd(M, C), rnd(M, C)
+        nw, gate = rnd(C), rnd(3, C)
+        nd = ccv3d.make_norm_desc(rows=M, C=C, post="rms", act="silu", gate_rows=M // 3)
+        pd = ccv3d.make_pointwise_desc(pixels=M, Cin=K, Cout=C, act="silu")
+        qd = ccv3d.make_qcache_desc(N=1, H=60, W=100, C=C, ring_slots=2, format="e4m3")
+        ws = [ccv3d.alloc_workspace(n) for n in (ccv3d.ccv3d_norm_workspace(nd),
+                                                 *ccv3d.ccv3d_pointwise_workspace(pd))]
+        codes, scales = ccv3d.alloc_qcache(qd)
+        out, pre, h, y, dh, db, dg, dw2, back = (torch.empty_like(t) for t in (
+            res, res, res, res, res, res, gate, nw, res))
+        dx, dw, dbias = torch.empty_like(x), torch.empty_like(w), torch.empty_like(nw)
+
+        def run(stream=None):
+            ccv3d.ccv3d_pointwise_forward(pd, x, w, nw, res, out, pre, ws[1], stream)
+            ccv3d.ccv3d_norm_forward(nd, res, out, gate, nw, None, nw, None, h, y, stream)
+            ccv3d.ccv3d_qcache_write(qd, y, 1, 0, 1, 1, codes, scales, stream)
+            ccv3d.ccv3d_qcache_read(qd, codes, scales, 1, 1, back, stream)
+            ccv3d.ccv3d_norm_backward(nd, h, out, gate, nw, None, nw, None, dout, res, dh, db, dg,
+                                      dw2, None, None, None, ws[0], stream)
+            ccv3d.ccv3d_pointwise_backward(pd, x, w, pre, db, dx, dw, dbias, ws[2], stream)
+            return [out, pre, h, y, back, dh, db, dg, dw2, dx, dw, dbias]
+
+        return run
+
+    jobs = [job(1), job(2)]
+    want = [[t.clone() for t in j()] for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(20):
+        got = [j(s) for j, s in zip(jobs, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("which", ["norm", "pointwise", "qcache"])
+def test_first_call_of_a_process_inside_a_capture(which):
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys, torch
+from causal_conv3d_video_b200 import ccv3d
+bf = lambda *s: torch.randn(s, device="cuda").bfloat16()
+if sys.argv[1] == "norm":
+    h, w = bf(1000, 96), bf(96)
+    out = [torch.empty_like(h), torch.empty_like(h), torch.empty_like(w)]
+    d = ccv3d.make_norm_desc(rows=1000, C=96, act="silu")
+    ws = ccv3d.alloc_workspace(ccv3d.ccv3d_norm_workspace(d))
+    def call():
+        ccv3d.ccv3d_norm_forward(d, h, None, None, None, None, w, None, None, out[0])
+        ccv3d.ccv3d_norm_backward(d, h, None, None, None, None, w, None, h, None, out[1], None,
+                                  None, None, None, out[2], None, ws)
+elif sys.argv[1] == "pointwise":
+    x, w = bf(1000, 192), bf(96, 192)
+    out = [bf(1000, 96), torch.empty_like(x), torch.empty_like(w)]
+    d = ccv3d.make_pointwise_desc(pixels=1000, Cin=192, Cout=96)
+    ws = [ccv3d.alloc_workspace(n) for n in ccv3d.ccv3d_pointwise_workspace(d)]
+    def call():
+        ccv3d.ccv3d_pointwise_forward(d, x, w, None, None, out[0], None, ws[0])
+        ccv3d.ccv3d_pointwise_backward(d, x, w, None, out[0], out[1], out[2], None, ws[1])
+else:
+    x = bf(1, 1, 8, 8, 96)
+    d = ccv3d.make_qcache_desc(N=1, H=8, W=8, C=96, ring_slots=2)
+    out = [torch.empty_like(x), *ccv3d.alloc_qcache(d)]
+    def call():
+        ccv3d.ccv3d_qcache_write(d, x, 1, 0, 1, 1, out[1], out[2])
+        ccv3d.ccv3d_qcache_read(d, out[1], out[2], 1, 1, out[0])
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    call()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in out]
+call()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, out))
+assert ccv3d.ccv3d_block_get_status() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code, which], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
