@@ -332,20 +332,25 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(
     };
     auto load = [&](long long row, Row& r) {
         const long long at = row * C;
-        const bool ok = row < row1 && in_bounds(&g_block_status, static_cast<const T*>(p.h) + at,
-                                                (long long)C * sizeof(T), p.h, tensor);
+        const bool ok = row < row1;
+        // (each tensor by itself: the call may go without any of them)
+        auto there = [&](const void* base) {
+            return in_bounds(&g_block_status, static_cast<const T*>(base) + at,
+                             (long long)C * sizeof(T), base, tensor);
+        };
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
             const int c0 = unit_c0<V>(u, lane, tpr);
             zero8<T, V>(r.h[u]); zero8<T, V>(r.y[u]); zero8<T, V>(r.g[u]); zero8<T, V>(r.b[u]);
             if (!ok) continue;
-            if (has_pre) {
+            if (has_pre && there(p.h) && there(p.dy)) {
                 load8<T, V>(r.h[u], static_cast<const T*>(p.h) + at, c0, tpr, C);
                 load8<T, V>(r.y[u], static_cast<const T*>(p.dy) + at, c0, tpr, C);
             }
-            if (p.dh_out != nullptr)
+            if (p.dh_out != nullptr && there(p.dh_out))
                 load8<T, V>(r.g[u], static_cast<const T*>(p.dh_out) + at, c0, tpr, C);
-            if (has_b) load8<T, V>(r.b[u], static_cast<const T*>(p.b) + at, c0, tpr, C);
+            if (has_b && there(p.b))
+                load8<T, V>(r.b[u], static_cast<const T*>(p.b) + at, c0, tpr, C);
         }
     };
     const long long stride = p.blocks_per_group;

@@ -276,6 +276,19 @@ def test_backward_parts_and_long():
     _check_backward(_case(333, 40, "fp32", actk="gelu"), dh_out=False)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("C", [96, 75, 1024, 1001, 5000])
+def test_backward_without_the_stream(C, dtype):
+    """Without a pre norm the stream's value is not read, and may be NULL."""
+    cases = [_case(90, C, dtype, pre="none", post="rms", residual=True, gates=3, seed=5)
+             for _ in range(3)]
+    want = _backward(cases[0])[2]
+    got = _backward(dict(cases[1], h=None))[2]
+    assert set(got) == set(want) - {"dh"}
+    assert all(torch.equal(got[k], want[k]) for k in got)
+    _check_backward(cases[2])
+
+
 def test_backward_same_bits_every_run():
     for C in (96, 75, 1536):
         s = _case(5000, C, "bf16", residual=True, gates=5, post="rms", actk="silu", bias=True)
