@@ -521,6 +521,17 @@ __device__ __forceinline__ void tile_tail(const TileSpan& t, const void* const (
     __syncthreads();
 }
 
+// Waits for a tile; false from the first wait that ran out on.  After that the
+// thread stores nothing, and issues nothing where it is the issuing one; `waits`
+// counts down from the number of stages, a wait each that ran out, so that the
+// tiles issued before are all waited for (the stages - 1 that follow: no copy
+// lands in shared memory that has become another block's) and the waits for the
+// ones never issued end soon.
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t ph, int stages, int& waits) {
+    if (waits > 0 && !mbar_wait(smem_u32(bar), ph, &g_block_status, kWaitLimitNs)) --waits;
+    return waits == stages;
+}
+
 // Eight channels of a vector kept in shared memory, as pairs.
 __device__ __forceinline__ void vec8(f2 (&f)[4], const float* s, bool vec, int c0, int step) {
     if (vec) {
@@ -639,9 +650,9 @@ __global__ void __launch_bounds__(kTileThreads, 3) norm_fwd_tiles(
     const bool post_bias = p.post_bias != nullptr, pre_bias = p.pre_bias != nullptr;
     int st = 0;
     uint32_t ph = 0;
-    bool live = true;
+    int waits = sh.stages;  // (see tile_wait)
     for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
-        if (live && !mbar_wait(smem_u32(&full[st]), ph, &g_block_status, kWaitLimitNs)) live = false;
+        const bool live = tile_wait(&full[st], ph, sh.stages, waits);
         uint8_t* stage = ring + st * stage_bytes;
         const TileSpan sp = span(t);
         tile_tail<nT>(sp, src, stage, sh.cap);
@@ -714,7 +725,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) norm_fwd_tiles(
             }
         }
         __syncthreads();  // every thread is done with the stage
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 0 && live) {
             const long long nt = t + (long long)sh.stages * gridDim.x;
             if (nt < tiles)
                 tile_issue<nT>(span(nt), src, stage, sh.cap, smem_u32(&full[st]), tensor);
@@ -786,9 +797,9 @@ __global__ void __launch_bounds__(kTileThreads, bwd_blocks(kForm, NU)) norm_bwd_
             for (int i = 0; i < 4; ++i) acc[q][u][i] = f2_all(0.0f);
     int st = 0;
     uint32_t ph = 0;
-    bool live = true;
+    int waits = sh.stages;  // (see tile_wait)
     for (long long t = part_of; t < tiles; t += p.blocks_per_group) {
-        if (live && !mbar_wait(smem_u32(&full[st]), ph, &g_block_status, kWaitLimitNs)) live = false;
+        const bool live = tile_wait(&full[st], ph, sh.stages, waits);
         uint8_t* stage = ring + st * stage_bytes;
         const TileSpan sp = span(t);
         tile_tail<nT>(sp, src, stage, sh.cap);
@@ -911,7 +922,7 @@ __global__ void __launch_bounds__(kTileThreads, bwd_blocks(kForm, NU)) norm_bwd_
             }
         }
         __syncthreads();  // every thread is done with the stage
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 0 && live) {
             const long long nt = t + (long long)sh.stages * p.blocks_per_group;
             if (nt < tiles)
                 tile_issue<nT>(span(nt), src, stage, sh.cap, smem_u32(&full[st]), tensor);
@@ -921,6 +932,7 @@ __global__ void __launch_bounds__(kTileThreads, bwd_blocks(kForm, NU)) norm_bwd_
             ph ^= 1u;
         }
     }
+    if (!__syncthreads_and(waits == sh.stages)) return;  // a wait ran out
     float sums[kQ][NU][8];
 #pragma unroll
     for (int q = 0; q < kQ; ++q)

@@ -408,7 +408,10 @@ __global__ void __launch_bounds__(256) pw_rows_mma_kernel(const bf16_t* x, const
 #pragma unroll
     for (int m = 0; m < MB; ++m) xr[m] = x + (long long)(m * 8 + g < M ? m * 8 + g : 0) * K;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    bool live = true;
+    // kRwStages until a wait runs out.  From then on nothing more is issued or
+    // stored, and the waits left cover the chunks issued before: no copy lands in
+    // shared memory that has become another block's.
+    int waits = kRwStages;
     for (int c = 0; c < chunks; ++c) {
         // this thread's two 32-wide steps of the chunk; x is read before the wait
         uint4 rx[2][kTiles * 2];
@@ -422,9 +425,9 @@ __global__ void __launch_bounds__(256) pw_rows_mma_kernel(const bf16_t* x, const
                                ? *reinterpret_cast<const uint4*>(xr[m < MB ? m : 0] + k) : zero;
         }
         const int st = c % kRwStages;
-        if (live && !mbar_wait(smem_u32(&full[st]), (uint32_t)(c / kRwStages & 1), &g_block_status,
-                               kWaitLimitNs))
-            live = false;
+        if (waits > 0 && !mbar_wait(smem_u32(&full[st]), (uint32_t)(c / kRwStages & 1),
+                                    &g_block_status, kWaitLimitNs))
+            --waits;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int kk = (u * 8 + warp) * 32 + t * 8;
@@ -440,7 +443,7 @@ __global__ void __launch_bounds__(256) pw_rows_mma_kernel(const bf16_t* x, const
         }
         if (c + kRwStages < chunks) {
             __syncthreads();  // every warp is done with the chunk
-            if (threadIdx.x == 0) issue(c + kRwStages);
+            if (threadIdx.x == 0 && waits == kRwStages) issue(c + kRwStages);
         }
     }
     // d0, d1: row g, channels 2t and 2t + 1; d2, d3: row g + 8
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(256) pw_rows_mma_kernel(const bf16_t* x, const
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             part[warp][m * 16 + g + (i >> 1) * 8][2 * t + (i & 1)] = acc[m][i];
-    __syncthreads();
+    if (!__syncthreads_and(waits == kRwStages)) return;  // a wait ran out
     for (int i = threadIdx.x; i < kTiles * 128; i += 256) {
         const int n = i & 7, m = i >> 3;  // channels side by side
         if (m >= M || n0 + n >= o.N) continue;

@@ -476,9 +476,8 @@ CCV3D_API ccv3d_status ccv3d_forward_qring(ccv3d_plan_t plan, const void* x,
 /* Status of the ccv3d_norm_*, ccv3d_pointwise_* and ccv3d_qcache_* calls on the
  * current device: waits for the work queued on `stream`, then returns and
  * clears the first error their kernels recorded on the device -- CCV3D_OK,
- * CCV3D_ERR_TIMEOUT (a bounded wait of the tensor-core product ran out: that
- * call's output is not valid) or, in the bounds-checked build,
- * CCV3D_ERR_BOUNDS.  Allocates nothing.  Errors: CUDA. */
+ * CCV3D_ERR_TIMEOUT (a bounded wait of a norm or a product ran out: that call's
+ * outputs are not valid) or, in the bounds-checked build, CCV3D_ERR_BOUNDS.  Allocates nothing.  Errors: CUDA. */
 CCV3D_API ccv3d_status ccv3d_block_get_status(cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
