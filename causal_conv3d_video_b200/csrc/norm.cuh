@@ -157,16 +157,22 @@ __global__ void __launch_bounds__(512) norm_fwd_rows(
     const int C = p.C;
     const long long tensor = p.rows * C * (long long)sizeof(T), stride = gridDim.x;
     const T *h = static_cast<const T*>(p.h), *b = static_cast<const T*>(p.b);
+    // (checked build) the row at element `at` of a tensor lies in it
+    auto fits = [&](const void* base, long long at) {
+        return in_bounds(&g_block_status, static_cast<const T*>(base) + at,
+                         (long long)C * sizeof(T), base, tensor);
+    };
     // what each thread keeps of the vectors
     float w[NU][8], wb[NU][8], g[NU][8], gb[NU][8];
     long long gate_row = -1;
     auto gates = [&](long long row) {  // scale * gate * post_w, scale * gate * post_bias
+        const T* gate = static_cast<const T*>(p.gate);
+        if (gate != nullptr && index_ok(&g_block_status, row, p.rows / p.gate_rows)) gate += row * C;
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
             const int c0 = unit_c0<V>(u, lane, tpr);
             float t[8];
-            weights8<T, V>(t, p.gate == nullptr ? nullptr : static_cast<const T*>(p.gate) + row * C,
-                           1.0f, c0, tpr, C);
+            weights8<T, V>(t, gate, 1.0f, c0, tpr, C);
             weights8<T, V>(g[u], static_cast<const T*>(p.post_w), 1.0f, c0, tpr, C);
             weights8<T, V>(gb[u], static_cast<const T*>(p.post_bias), 0.0f, c0, tpr, C);
 #pragma unroll
@@ -187,15 +193,14 @@ __global__ void __launch_bounds__(512) norm_fwd_rows(
                            unit_c0<V>(u, lane, tpr), tpr, C);
         }
     auto load = [&](long long row, Raw8<T, V> (&rh)[NU], Raw8<T, V> (&rb)[NU]) {
-        const bool ok = row < p.rows &&
-                        in_bounds(&g_block_status, h + row * C, (long long)C * sizeof(T), p.h, tensor);
+        const bool ok = row < p.rows;
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
             const int c0 = unit_c0<V>(u, lane, tpr);
-            if (ok) load8<T, V>(rh[u], h + row * C, c0, tpr, C);
+            if (ok && fits(h, row * C)) load8<T, V>(rh[u], h + row * C, c0, tpr, C);
             else zero8<T, V>(rh[u]);
             if constexpr (kB) {
-                if (ok) load8<T, V>(rb[u], b + row * C, c0, tpr, C);
+                if (ok && fits(b, row * C)) load8<T, V>(rb[u], b + row * C, c0, tpr, C);
                 else zero8<T, V>(rb[u]);
             }
         }
@@ -206,7 +211,6 @@ __global__ void __launch_bounds__(512) norm_fwd_rows(
     for (; row < p.rows; row += stride) {
         Raw8<T, V> nh[NU], nb[NU];
         load(row + stride, nh, nb);
-        constexpr bool ok = true;
         const long long at = row * C;
         float v[NU][8];
 #pragma unroll
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(512) norm_fwd_rows(
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[u][i] += fmaf(m[u][i], g[u][i], gb[u][i]);
                 const Raw8<T, V> r = pack8<T, V>(v[u]);
-                if (ok) store8<T, V>(r, static_cast<T*>(p.h_out) + at, c0, tpr, C);
+                if (fits(p.h_out, at)) store8<T, V>(r, static_cast<T*>(p.h_out) + at, c0, tpr, C);
                 unpack8<T, V>(r, v[u]);  // the stored value is what the norm reads
             }
         }
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(512) norm_fwd_rows(
                 if (p.act != kActNone)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[u][i] = act_of<T>(v[u][i], p.act);
-                if (ok)
+                if (fits(p.y, at))
                     store8<T, V>(pack8<T, V>(v[u]), static_cast<T*>(p.y) + at,
                                  unit_c0<V>(u, lane, tpr), tpr, C);
             }
@@ -313,6 +317,7 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(
     const int part_of = (int)(blockIdx.x % p.blocks_per_group);
     const long long row0 = group * p.group_rows, row1 = row0 + p.group_rows;
     const bool has_pre = p.dy != nullptr, has_b = p.b != nullptr;
+    const long long gate_at = index_ok(&g_block_status, group, p.groups) ? group * C : 0;
     float w[NU][8], wb[NU][8], g[NU][8];  // pre_w, pre_bias, scale * gate * post_w
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
@@ -321,8 +326,8 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(
         if constexpr (kGen)
             weights8<T, V>(wb[u], static_cast<const T*>(p.pre_bias), 0.0f, c0, tpr, C);
         float t[8];
-        weights8<T, V>(t, p.gate == nullptr ? nullptr : static_cast<const T*>(p.gate) + group * C,
-                       1.0f, c0, tpr, C);
+        weights8<T, V>(t, p.gate == nullptr ? nullptr : static_cast<const T*>(p.gate) + gate_at, 1.0f,
+                       c0, tpr, C);
         weights8<T, V>(g[u], static_cast<const T*>(p.post_w), 1.0f, c0, tpr, C);
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[u][i] *= p.scale * t[i];
@@ -330,26 +335,27 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(
     struct Row {
         Raw8<T, V> h[NU], y[NU], g[NU], b[NU];
     };
+    // (checked build) the row at element `at` of a tensor lies in it; each tensor
+    // by itself, since the call may go without any of them
+    auto fits = [&](const void* base, long long at) {
+        return in_bounds(&g_block_status, static_cast<const T*>(base) + at,
+                         (long long)C * sizeof(T), base, tensor);
+    };
     auto load = [&](long long row, Row& r) {
         const long long at = row * C;
         const bool ok = row < row1;
-        // (each tensor by itself: the call may go without any of them)
-        auto there = [&](const void* base) {
-            return in_bounds(&g_block_status, static_cast<const T*>(base) + at,
-                             (long long)C * sizeof(T), base, tensor);
-        };
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
             const int c0 = unit_c0<V>(u, lane, tpr);
             zero8<T, V>(r.h[u]); zero8<T, V>(r.y[u]); zero8<T, V>(r.g[u]); zero8<T, V>(r.b[u]);
             if (!ok) continue;
-            if (has_pre && there(p.h) && there(p.dy)) {
+            if (has_pre && fits(p.h, at) && fits(p.dy, at)) {
                 load8<T, V>(r.h[u], static_cast<const T*>(p.h) + at, c0, tpr, C);
                 load8<T, V>(r.y[u], static_cast<const T*>(p.dy) + at, c0, tpr, C);
             }
-            if (p.dh_out != nullptr && there(p.dh_out))
+            if (p.dh_out != nullptr && fits(p.dh_out, at))
                 load8<T, V>(r.g[u], static_cast<const T*>(p.dh_out) + at, c0, tpr, C);
-            if (has_b && there(p.b))
+            if (has_b && fits(p.b, at))
                 load8<T, V>(r.b[u], static_cast<const T*>(p.b) + at, c0, tpr, C);
         }
     };
@@ -360,7 +366,6 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(
     for (; row < row1; row += stride) {
         Row next;
         load(row + stride, next);
-        constexpr bool ok = true;
         const long long at = row * C;
         float G[NU][8];
 #pragma unroll
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(
                 for (int i = 0; i < 8; ++i)
                     G[u][i] = fmaf(rstd, fmaf(n[u][i], a, kGen ? d[u][i] - mean : d[u][i]), G[u][i]);
         }
-        if (p.dh != nullptr && ok)
+        if (p.dh != nullptr && fits(p.dh, at))
 #pragma unroll
             for (int u = 0; u < NU; ++u)
                 store8<T, V>(pack8<T, V>(G[u]), static_cast<T*>(p.dh) + at,
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(512) norm_bwd_rows(
                         for (int i = 0; i < 8; ++i)
                             G[u][i] = rstd * fmaf(m[u][i], a, kGen ? G[u][i] - mean : G[u][i]);
                 }
-                if (ok)
+                if (fits(p.db, at))
 #pragma unroll
                     for (int u = 0; u < NU; ++u)
                         store8<T, V>(pack8<T, V>(G[u]), static_cast<T*>(p.db) + at,
@@ -510,12 +515,13 @@ __device__ __forceinline__ void tile_issue(const TileSpan& t, const void* const 
 // The bytes after the bulk copies (all threads; uniform).
 template <int nT>
 __device__ __forceinline__ void tile_tail(const TileSpan& t, const void* const (&src)[nT],
-                                          uint8_t* stage, int cap) {
+                                          uint8_t* stage, int cap, long long tensor) {
     if (t.tail == 0) return;
     if ((int)threadIdx.x < t.tail)
 #pragma unroll
         for (int k = 0; k < nT; ++k)
-            if (src[k] != nullptr)
+            if (src[k] != nullptr &&
+                index_ok(&g_block_status, t.from + t.bulk + (int)threadIdx.x, tensor))
                 stage[(size_t)k * cap + t.bulk + threadIdx.x] =
                     static_cast<const uint8_t*>(src[k])[t.from + t.bulk + threadIdx.x];
     __syncthreads();
@@ -646,6 +652,10 @@ __global__ void __launch_bounds__(kTileThreads, 3) norm_fwd_tiles(
         vecs[3 * L + c] = g * vec_at<T>(p.post_bias, c, C, 0.0f);
     }
     __syncthreads();
+    // (checked build) the row at element `at` of a tensor lies in it
+    auto fits = [&](const void* base, long long at) {
+        return in_bounds(&g_block_status, static_cast<const T*>(base) + at, row_bytes, base, tensor);
+    };
     const bool gated = kB && p.gate != nullptr && p.gate_rows < p.rows;
     const bool post_bias = p.post_bias != nullptr, pre_bias = p.pre_bias != nullptr;
     int st = 0;
@@ -655,7 +665,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) norm_fwd_tiles(
         const bool live = tile_wait(&full[st], ph, sh.stages, waits);
         uint8_t* stage = ring + st * stage_bytes;
         const TileSpan sp = span(t);
-        tile_tail<nT>(sp, src, stage, sh.cap);
+        tile_tail<nT>(sp, src, stage, sh.cap, tensor);
         const int n = (int)min((long long)sh.rows, p.rows - t * sh.rows);
         for (int r0 = 0; r0 < n; r0 += rpp) {
             const int r = r0 + sub;
@@ -672,7 +682,9 @@ __global__ void __launch_bounds__(kTileThreads, 3) norm_fwd_tiles(
                     tile_unit<T, V, TPR>(m[u], in + sh.cap, u, lane, C, ok);
                 if (p.post != kNormNone)
                     normalise2<V, TPR, NU>(m, p.post, lane, C, p.eps, p.inv_c);
-                const T* gate = static_cast<const T*>(p.gate) + (gated && ok ? row / p.gate_rows * C : 0);
+                const long long gate_row = gated && ok ? row / p.gate_rows : 0;
+                const T* gate = static_cast<const T*>(p.gate) +
+                                (index_ok(&g_block_status, gate_row, p.rows / p.gate_rows) ? gate_row * C : 0);
 #pragma unroll
                 for (int u = 0; u < NU; ++u) {
                     const int c0 = unit_c0<V>(u, lane, TPR);
@@ -695,7 +707,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) norm_fwd_tiles(
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[u][i] = f2_add(v[u][i], m[u][i]);
                     const Raw8<T, V> o = pack8<T, V>(v[u]);
-                    if (ok) store8<T, V>(o, static_cast<T*>(p.h_out) + at, c0, TPR, C);
+                    if (ok && fits(p.h_out, at)) store8<T, V>(o, static_cast<T*>(p.h_out) + at, c0, TPR, C);
                     unpack8<T, V>(o, v[u]);  // the stored value is what the norm reads
                 }
             }
@@ -720,7 +732,8 @@ __global__ void __launch_bounds__(kTileThreads, 3) norm_fwd_tiles(
 #pragma unroll
                         for (int i = 0; i < 4; ++i) v[u][i] = f2_act<T>(v[u][i], kActGelu);
                     }
-                    if (ok) store8<T, V>(pack8<T, V>(v[u]), static_cast<T*>(p.y) + at, c0, TPR, C);
+                    if (ok && fits(p.y, at))
+                        store8<T, V>(pack8<T, V>(v[u]), static_cast<T*>(p.y) + at, c0, TPR, C);
                 }
             }
         }
@@ -781,7 +794,12 @@ __global__ void __launch_bounds__(kTileThreads, bwd_blocks(kForm, NU)) norm_bwd_
                 tile_issue<nT>(span(t), src, ring + s * stage_bytes, sh.cap, smem_u32(&full[s]), tensor);
         }
     }
-    const T* gate = p.gate == nullptr ? nullptr : static_cast<const T*>(p.gate) + group * C;
+    // (checked build) the row at element `at` of a tensor lies in it
+    auto fits = [&](const void* base, long long at) {
+        return in_bounds(&g_block_status, static_cast<const T*>(base) + at, row_bytes, base, tensor);
+    };
+    const T* gate = static_cast<const T*>(p.gate);
+    if (gate != nullptr && index_ok(&g_block_status, group, p.groups)) gate += group * C;
     for (int c = threadIdx.x; c < L; c += blockDim.x) {
         vecs[c] = vec_at<T>(p.pre_w, c, C, 1.0f);
         vecs[L + c] = vec_at<T>(p.pre_bias, c, C, 0.0f);
@@ -802,7 +820,7 @@ __global__ void __launch_bounds__(kTileThreads, bwd_blocks(kForm, NU)) norm_bwd_
         const bool live = tile_wait(&full[st], ph, sh.stages, waits);
         uint8_t* stage = ring + st * stage_bytes;
         const TileSpan sp = span(t);
-        tile_tail<nT>(sp, src, stage, sh.cap);
+        tile_tail<nT>(sp, src, stage, sh.cap, tensor);
         const int n = (int)min((long long)sh.rows, p.group_rows - t * sh.rows);
         for (int r0 = 0; r0 < n; r0 += rpp) {
             const int r = r0 + sub;
@@ -867,7 +885,7 @@ __global__ void __launch_bounds__(kTileThreads, bwd_blocks(kForm, NU)) norm_bwd_
                 for (int u = 0; u < NU; ++u)
                     tile_unit<T, V, TPR>(G[u], in + 2 * sh.cap, u, lane, C, ok);
             }
-            if (p.dh != nullptr && ok)
+            if (p.dh != nullptr && ok && fits(p.dh, at))
 #pragma unroll
                 for (int u = 0; u < NU; ++u)
                     store8<T, V>(pack8<T, V>(G[u]), static_cast<T*>(p.dh) + at,
@@ -913,7 +931,7 @@ __global__ void __launch_bounds__(kTileThreads, bwd_blocks(kForm, NU)) norm_bwd_
                                 G[u][i] = f2_mul(r2, f2_fma(v[u][i], a,
                                                             kMean ? f2_add(G[u][i], mean) : G[u][i]));
                     }
-                    if (ok)
+                    if (ok && fits(p.db, at))
 #pragma unroll
                         for (int u = 0; u < NU; ++u)
                             store8<T, V>(pack8<T, V>(G[u]), static_cast<T*>(p.db) + at,
@@ -1026,7 +1044,7 @@ __global__ void __launch_bounds__(1024) norm_fin_group_kernel(const __grid_const
             put<T>(p.dpre_bias, c, s[2]);
             put<T>(p.dpost_bias, c, s[3]);
         } else {
-            for (int q = 0; q < nq; ++q)
+            for (int q = 0; q < nq && index_ok(&g_block_status, g * p.blocks_per_group, p.slots); ++q)
                 p.part_out[((long long)q * p.slots + g * p.blocks_per_group) * C + c] = s[q];
         }
     }

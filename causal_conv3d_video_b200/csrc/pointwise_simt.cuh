@@ -227,7 +227,9 @@ __global__ void __launch_bounds__(256, SM * SN == 128 * 128 ? 2 : 4) pw_simt_ker
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const long long m = mh + r + j * kStep;
-                res[j] = residual != nullptr && m < p.M ? (float)residual[m * o.N + n] : 0.0f;
+                res[j] = residual != nullptr && m < p.M &&
+                                 in_bounds(&g_block_status, residual + m * o.N + n, sizeof(T), residual, bytes)
+                             ? (float)residual[m * o.N + n] : 0.0f;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -250,6 +252,7 @@ __global__ void __launch_bounds__(256) pw_join_kernel(const float* partial, int 
     const int per = ldp / 4;
     const long long total = o.M * per, step = (long long)gridDim.x * blockDim.x;
     const T *bias = static_cast<const T*>(o.bias), *residual = static_cast<const T*>(o.residual);
+    const long long bytes = o.M * o.N * (long long)sizeof(T);
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
         const long long m = i / per;
         const int n = (int)(i - m * per) * 4;
@@ -257,7 +260,9 @@ __global__ void __launch_bounds__(256) pw_join_kernel(const float* partial, int 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool in = n + j < o.N;
-            res[j] = in && residual != nullptr ? (float)residual[m * o.N + n + j] : 0.0f;
+            res[j] = in && residual != nullptr &&
+                             in_bounds(&g_block_status, residual + m * o.N + n + j, sizeof(T), residual, bytes)
+                         ? (float)residual[m * o.N + n + j] : 0.0f;
             b[j] = in && bias != nullptr ? (float)bias[n + j] : 0.0f;
         }
         const float* src = partial + m * ldp + n;
@@ -272,9 +277,7 @@ __global__ void __launch_bounds__(256) pw_join_kernel(const float* partial, int 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             T* out = static_cast<T*>(o.out) + m * o.N + n + j;
-            if (n + j >= o.N || !in_bounds(&g_block_status, out, sizeof(T), o.out,
-                                           o.M * o.N * (long long)sizeof(T)))
-                continue;
+            if (n + j >= o.N || !in_bounds(&g_block_status, out, sizeof(T), o.out, bytes)) continue;
             u[j] += b[j];
             if (o.pre != nullptr) static_cast<T*>(o.pre)[m * o.N + n + j] = (T)u[j];
             *out = (T)(act_of<T>(u[j], o.act) + res[j]);
@@ -317,7 +320,11 @@ __global__ void __launch_bounds__(256) pw_rows_kernel(const T* x, const T* w, in
             if (m >= M) break;
             Raw8<T, V> rx;
             f2 g[4];
-            load8<T, V>(rx, x + (long long)m * K, c0, 32, K);
+            const T* row = x + (long long)m * K;
+            if (in_bounds(&g_block_status, row, (long long)K * sizeof(T), x, M * (long long)K * sizeof(T)))
+                load8<T, V>(rx, row, c0, 32, K);
+            else
+                zero8<T, V>(rx);
             unpack8<T, V>(rx, g);
 #pragma unroll
             for (int c = 0; c < CPW; ++c) {
@@ -490,6 +497,7 @@ __global__ void __launch_bounds__(256) pw_dact_kernel(const T* pre, const T* dou
             if (at < r1 && in_bounds(&g_block_status, dout + at * N, (long long)N * sizeof(T), dout,
                                      M * N * (long long)sizeof(T))) {
                 load8<T, V>(rd[j], dout + at * N, c0, tpr, N);
+                // (pre has the extent of dout)
                 if (pre != nullptr) load8<T, V>(rp[j], pre + at * N, c0, tpr, N);
             }
         }
@@ -532,7 +540,9 @@ __global__ void __launch_bounds__(1024) pw_colsum_kernel(const float* part, int 
     const int c = blockIdx.x * 32 + threadIdx.x;
     float a = 0.0f;
     if (c < N)
-        for (int i = threadIdx.y; i < chunks; i += 32) a += part[(long long)i * N + c];
+        for (int i = threadIdx.y; i < chunks; i += 32)
+            if (index_ok(&g_block_status, (long long)i * N + c, (long long)chunks * N))
+                a += part[(long long)i * N + c];
     buf[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
     if (threadIdx.y == 0 && c < N) {

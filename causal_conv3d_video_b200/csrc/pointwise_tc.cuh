@@ -596,7 +596,8 @@ __global__ void __launch_bounds__(256) pw_pack_kernel(const bf16_t* src, bf16_t*
         if (!in_bounds(&g_block_status, src + r * C, C * 2LL, src, rows * C * 2)) continue;
         load8<bf16_t, false>(raw, src + r * C, c0, 1, C);
         unpack8<bf16_t, false>(raw, f);
-        *reinterpret_cast<uint4*>(dst + r * Cp + c0) = pack8<bf16_t, true>(f).a;
+        if (in_bounds(&g_block_status, dst + r * Cp + c0, 16, dst, rows * Cp * 2))
+            *reinterpret_cast<uint4*>(dst + r * Cp + c0) = pack8<bf16_t, true>(f).a;
     }
 }
 

@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(kQThreads) qcache_write_kernel(const __grid_co
     uint8_t* scales = p.scales + slot * p.pixels * p.groups;
     const long long x_bytes = (long long)p.N * p.T * p.pixels * p.C * (long long)sizeof(T);
     const long long s_bytes = (long long)p.N * p.slots * p.pixels * p.groups;
+    const long long c_bytes = (long long)p.N * p.slots * p.pixels * p.code_bytes;
     const int per = p.groups * 4;  // threads a pixel
     const long long units = p.pixels * per;
     const long long u0 = (long long)blockIdx.x * (kQThreads * kQUnits) + threadIdx.x;
@@ -327,12 +328,17 @@ __global__ void __launch_bounds__(kQThreads) qcache_write_kernel(const __grid_co
             uint8_t* out = kFlat ? codes : codes + at[k].px * p.code_bytes;
             const long long o = kFlat ? u * 8 : c0;
             if (kFlat || c0 < p.C) {
-                if (fmt == kQE2m1) *reinterpret_cast<uint32_t*>(out + o / 2) = w.x;
-                else *reinterpret_cast<uint2*>(out + o) = w;
+                if (fmt == kQE2m1) {
+                    if (in_bounds(&g_block_status, out + o / 2, 4, p.codes, c_bytes))
+                        *reinterpret_cast<uint32_t*>(out + o / 2) = w.x;
+                } else if (in_bounds(&g_block_status, out + o, 8, p.codes, c_bytes)) {
+                    *reinterpret_cast<uint2*>(out + o) = w;
+                }
             }
         } else if (c0 < p.C) {
-            uint8_t* out = codes + at[k].px * p.code_bytes + (fmt == kQE2m1 ? c0 / 2 : c0);
-            put_codes<W>(w, out, p.C - c0, fmt == kQE2m1);
+            uint8_t* row_codes = codes + at[k].px * p.code_bytes;
+            if (in_bounds(&g_block_status, row_codes, p.code_bytes, p.codes, c_bytes))
+                put_codes<W>(w, row_codes + (fmt == kQE2m1 ? c0 / 2 : c0), p.C - c0, fmt == kQE2m1);
         }
     }
 }
@@ -347,6 +353,7 @@ __global__ void __launch_bounds__(kQThreads) qcache_read_kernel(const __grid_con
     const uint8_t* scales = p.scales + slot * p.pixels * p.groups;
     const long long o_bytes = (long long)p.N * p.frames * p.pixels * p.C * (long long)sizeof(T);
     const long long s_bytes = (long long)p.N * p.slots * p.pixels * p.groups;
+    const long long c_bytes = (long long)p.N * p.slots * p.pixels * p.code_bytes;
     const int per = (p.C + 7) / 8;  // threads a pixel
     const long long units = p.pixels * per;
     const long long u0 = (long long)blockIdx.x * (kQThreads * kQUnits) + threadIdx.x;
@@ -362,9 +369,13 @@ __global__ void __launch_bounds__(kQThreads) qcache_read_kernel(const __grid_con
         const int c0 = at[k].r * 8;
         const uint8_t* in = codes + at[k].px * p.code_bytes;
         const uint8_t* sc = kFlat ? scales + (u >> 2) : scales + at[k].px * p.groups + (at[k].r >> 2);
+        // (checked build) the unit's code bytes: its own in a flat frame, its pixel's otherwise
+        const long long unit_bytes = fmt == kQE2m1 ? 4 : 8;
+        const uint8_t* from = kFlat ? codes + u * unit_bytes : in;
         w[k] = make_uint2(0u, 0u);
         c[k] = 1;
-        ok[k] = u < units && in_bounds(&g_block_status, sc, 1, p.scales, s_bytes);
+        ok[k] = u < units && in_bounds(&g_block_status, sc, 1, p.scales, s_bytes) &&
+                in_bounds(&g_block_status, from, kFlat ? unit_bytes : p.code_bytes, p.codes, c_bytes);
         if (!ok[k]) continue;
         c[k] = *sc;
         if constexpr (W == 8) {
