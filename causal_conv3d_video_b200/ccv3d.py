@@ -385,9 +385,16 @@ def _status(rc, where, check):
     return rc
 
 
-def _bytes(ws):
-    """Size of a workspace: a tensor of any type, or None."""
-    return 0 if ws is None else ws.numel() * ws.element_size()
+def _bytes(where, ws, given):
+    """Size of a workspace: a tensor of any type, None, or the `given` bytes at a
+    raw address."""
+    if ws is None:
+        return 0
+    if type(ws) is int:
+        if given is None:
+            raise ValueError(f"{where}: ws is a raw address, whose size ws_bytes has to say")
+        return given
+    return ws.numel() * ws.element_size()
 
 
 def ccv3d_norm_workspace(desc: ccv3d_norm_desc) -> int:
@@ -411,9 +418,10 @@ def ccv3d_norm_forward(desc: ccv3d_norm_desc, h, b, gate, post_w, post_bias, pre
 
 def ccv3d_norm_backward(desc: ccv3d_norm_desc, h_out, b, gate, post_w, post_bias, pre_w, pre_bias,
                         dy, dh_out, dh, db, dgate, dpost_w, dpost_bias, dpre_w, dpre_bias, ws,
-                        stream=None, check: bool = True) -> int:
+                        stream=None, check: bool = True, ws_bytes: int | None = None) -> int:
     """Gradients of ccv3d_norm_forward (None for those not wanted); ws: a
-    workspace of at least ccv3d_norm_workspace(desc) bytes."""
+    workspace of at least ccv3d_norm_workspace(desc) bytes (ws_bytes: the size of
+    one given as a raw address)."""
     C = desc.C
     n = desc.rows * C
     gates = n // max(1, desc.gate_rows) if gate is not None else 0
@@ -424,7 +432,7 @@ def ccv3d_norm_backward(desc: ccv3d_norm_desc, h_out, b, gate, post_w, post_bias
         ("dy", dy, n), ("dh_out", dh_out, n), ("dh", dh, n), ("db", db, n),
         ("dgate", dgate, gates), ("dpost_w", dpost_w, C), ("dpost_bias", dpost_bias, C),
         ("dpre_w", dpre_w, C), ("dpre_bias", dpre_bias, C)), (("ws", ws, None, None),))
-    return _status(lib.ccv3d_norm_backward(desc, *a, _bytes(ws), st), where, check)
+    return _status(lib.ccv3d_norm_backward(desc, *a, _bytes(where, ws, ws_bytes), st), where, check)
 
 
 def ccv3d_pointwise_workspace(desc: ccv3d_pointwise_desc):
@@ -436,26 +444,29 @@ def ccv3d_pointwise_workspace(desc: ccv3d_pointwise_desc):
 
 
 def ccv3d_pointwise_forward(desc: ccv3d_pointwise_desc, x, w, bias, residual, out, pre, ws,
-                            stream=None, check: bool = True) -> int:
+                            stream=None, check: bool = True, ws_bytes: int | None = None) -> int:
     """out = act(x w^T + bias) + residual; pre (None: not wanted) receives the
-    argument of act."""
+    argument of act.  ws_bytes: the size of a ws given as a raw address."""
     M, K, N = desc.pixels, desc.Cin, desc.Cout
     where = "ccv3d_pointwise_forward"
     a, st = _operands(where, desc.dtype, stream, (
         ("x", x, M * K), ("w", w, N * K), ("bias", bias, N), ("residual", residual, M * N),
         ("out", out, M * N), ("pre", pre, M * N)), (("ws", ws, None, None),))
-    return _status(lib.ccv3d_pointwise_forward(desc, *a, _bytes(ws), st), where, check)
+    return _status(lib.ccv3d_pointwise_forward(desc, *a, _bytes(where, ws, ws_bytes), st), where,
+                   check)
 
 
 def ccv3d_pointwise_backward(desc: ccv3d_pointwise_desc, x, w, pre, dout, dx, dw, dbias, ws,
-                             stream=None, check: bool = True) -> int:
-    """Gradients of ccv3d_pointwise_forward (None for those not wanted)."""
+                             stream=None, check: bool = True, ws_bytes: int | None = None) -> int:
+    """Gradients of ccv3d_pointwise_forward (None for those not wanted).  ws_bytes:
+    the size of a ws given as a raw address."""
     M, K, N = desc.pixels, desc.Cin, desc.Cout
     where = "ccv3d_pointwise_backward"
     a, st = _operands(where, desc.dtype, stream, (
         ("x", x, M * K), ("w", w, N * K), ("pre", pre, M * N), ("dout", dout, M * N),
         ("dx", dx, M * K), ("dw", dw, N * K), ("dbias", dbias, N)), (("ws", ws, None, None),))
-    return _status(lib.ccv3d_pointwise_backward(desc, *a, _bytes(ws), st), where, check)
+    return _status(lib.ccv3d_pointwise_backward(desc, *a, _bytes(where, ws, ws_bytes), st), where,
+                   check)
 
 
 def ccv3d_qcache_sizes(desc: ccv3d_qcache_desc):

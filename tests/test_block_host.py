@@ -263,3 +263,22 @@ def test_plan_forward_qring_checks_sizes():
 
 def test_strerror_names_every_status():
     assert all(ccv3d.ccv3d_strerror(s) != "unknown status" for s in range(10))
+
+
+def test_raw_workspace_addresses():
+    """A workspace given as an address needs its size, and is then the call's."""
+    nd = ccv3d.make_norm_desc(rows=64, C=96, post="rms", gate_rows=32)
+    pd = ccv3d.make_pointwise_desc(pixels=64, Cin=192, Cout=96, act="silu")
+    a = [_addr(i) for i in range(17)]
+    for call, desc, n, need in (
+            (ccv3d.ccv3d_norm_backward, nd, 17, ccv3d.ccv3d_norm_workspace(nd)),
+            (ccv3d.ccv3d_pointwise_forward, pd, 7, 0),
+            (ccv3d.ccv3d_pointwise_backward, pd, 8, ccv3d.ccv3d_pointwise_workspace(pd)[1])):
+        with pytest.raises(ValueError, match="ws_bytes"):
+            call(desc, *a[:n], stream=0, check=False)
+        if need:
+            assert call(desc, *a[:n], stream=0, check=False,
+                        ws_bytes=need - 1) == CCV3D_ERR_SCRATCH_LIMIT
+        b = list(a[:n])
+        b[-2] = b[0]    # an output on an input: refused after the workspace's size
+        assert call(desc, *b, stream=0, check=False, ws_bytes=need) == CCV3D_ERR_ALIAS
