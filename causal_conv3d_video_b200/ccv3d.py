@@ -8,7 +8,6 @@ the import of this module fails loudly: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -169,11 +168,20 @@ def ccv3d_strerror(status: int) -> str:
     return lib.ccv3d_strerror(int(status)).decode()
 
 
-def ccv3d_plan(desc: ccv3d_desc) -> ctypes.c_void_p:
-    h = ctypes.c_void_p()
+class ccv3d_plan_t(ctypes.c_void_p):
+    """A plan's handle, and the elements of its calls' tensors by name."""
+    elements = None
+
+
+def ccv3d_plan(desc: ccv3d_desc) -> ccv3d_plan_t:
+    h = ccv3d_plan_t()
     rc = lib.ccv3d_plan(ctypes.byref(h), ctypes.byref(desc))
     if rc != 0:
         raise CCV3DError(rc, "ccv3d_plan")
+    frame = desc.N * desc.H * desc.W * desc.Cin
+    h.elements = {"x": frame * desc.T_x, "cache_buf": frame * desc.cache_len,
+                  "w": desc.Cout * desc.kt * desc.kh * desc.kw * desc.Cin, "bias": desc.Cout,
+                  "out": ccv3d_plan_sizes(h)["out_bytes"] // (2 if desc.dtype == CCV3D_BF16 else 4)}
     return h
 
 
@@ -507,9 +515,13 @@ def ccv3d_qcache_read(desc: ccv3d_qcache_desc, codes, scales, head: int, frames:
 
 def ccv3d_forward_qring(plan, x, desc: ccv3d_qcache_desc, codes, scales, head: int, cache_buf, w,
                         bias, out, stride, pad, dilation, stream=None, check: bool = True):
-    """ccv3d_forward_ring with the ring held in 8 or 4 bits.  Returns (status,
-    next_head)."""
-    dt = desc.dtype
+    """ccv3d_forward_ring with the ring held in 8 or 4 bits.  Tensors
+    have to be of the sizes that the plan was made for (a plan given as a raw
+    handle is the caller's word for them).  Returns (status, next_head)."""
+    dt, sizes = desc.dtype, getattr(plan, "elements", None)
+    for name, t in (("x", x), ("cache_buf", cache_buf), ("w", w), ("bias", bias), ("out", out)):
+        if sizes and t is not None and type(t) is not int and t.numel() != sizes[name]:
+            raise ValueError(f"forward_qring: {name} has {t.numel()} elements, not {sizes[name]}")
     a, st = _operands("ccv3d_forward_qring", dt, stream, (), (
         ("x", x, None, dt), *_ring(desc, codes, scales), ("cache_buf", cache_buf, None, dt),
         ("w", w, None, dt), ("bias", bias, None, dt), ("out", out, None, dt)))
@@ -623,12 +635,6 @@ class Plan:
 
     def forward_qring(self, x, desc, codes, scales, head, cache_buf, w, bias, out, stream=None):
         """Call with its ring cache in 8 or 4 bits; returns the head of the new cache."""
-        d, frame = self.desc, self.desc.N * self.desc.H * self.desc.W * self.desc.Cin
-        for name, t, n in (("x", x, frame * d.T_x), ("cache_buf", cache_buf, frame * d.cache_len),
-                           ("w", w, d.Cout * d.kt * d.kh * d.kw * d.Cin), ("bias", bias, d.Cout),
-                           ("out", out, math.prod(self.out_shape()))):
-            if t is not None and not isinstance(t, int) and t.numel() != n:
-                raise ValueError(f"forward_qring: {name} has {t.numel()} elements, not {n}")
         return ccv3d_forward_qring(self.handle, x, desc, codes, scales, head, cache_buf, w, bias,
                                    out, self.stride, self.pad, self.dilation, stream)[1]
 

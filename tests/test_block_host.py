@@ -282,3 +282,22 @@ def test_raw_workspace_addresses():
         b = list(a[:n])
         b[-2] = b[0]    # an output on an input: refused after the workspace's size
         assert call(desc, *b, stream=0, check=False, ws_bytes=need) == CCV3D_ERR_ALIAS
+
+
+def test_forward_qring_checks_sizes():
+    """The call itself, not Plan's method alone."""
+    import torch
+    plan = ccv3d.ccv3d_plan(ccv3d.make_desc(N=1, Cin=96, Cout=32, H=4, W=6, T_x=1, cache_len=2))
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    good = dict(x=bf(1, 1, 4, 6, 96), cache_buf=bf(1, 2, 4, 6, 96), w=bf(32, 3, 3, 3, 96),
+                bias=bf(32), out=bf(1, 1, 4, 6, 32))
+    try:
+        for name in good:
+            for wrong in (good[name][..., :-8].contiguous(), torch.cat([good[name]] * 2)):
+                a = dict(good, **{name: wrong})
+                with pytest.raises(ValueError, match=f"{name} has {wrong.numel()} elements"):
+                    ccv3d.ccv3d_forward_qring(plan, a["x"], qdesc(), _addr(1), _addr(2), 0,
+                                              a["cache_buf"], a["w"], a["bias"], a["out"], (1, 1),
+                                              (1, 1), (1, 1, 1), stream=0)
+    finally:
+        ccv3d.ccv3d_destroy(plan)
