@@ -554,7 +554,7 @@ QCacheJob qcache_job(const ccv3d_qcache_desc* d) {
     return j;
 }
 
-// Whole frames on the grid's second axis (at most 65535 of them).
+// Whole frames on the grid's second axis (at most CCV3D_QCACHE_MAX_FRAMES of them).
 dim3 qcache_grid(const QCacheJob& j, long long threads_a_pixel) {
     return dim3((unsigned)up(j.pixels * threads_a_pixel, kQThreads * kQUnits),
                 (unsigned)(j.N * j.frames));
@@ -794,7 +794,7 @@ ccv3d_status ccv3d_qcache_write(const ccv3d_qcache_desc* d, const void* x, int T
         return CCV3D_ERR_INVALID;
     if ((long long)d->N * frames == 0) return CCV3D_OK;
     if (x == nullptr || codes == nullptr || scales == nullptr) return CCV3D_ERR_INVALID;
-    if ((long long)d->N * frames > 65535) return CCV3D_ERR_UNSUPPORTED;
+    if ((long long)d->N * frames > CCV3D_QCACHE_MAX_FRAMES) return CCV3D_ERR_UNSUPPORTED;
     QCacheJob j = qcache_job(d);
     Buffers bufs;
     bufs.in(x, (size_t)d->N * T_x * j.pixels * d->C * size_of(d->dtype));
@@ -823,7 +823,7 @@ ccv3d_status ccv3d_qcache_read(const ccv3d_qcache_desc* d, const void* codes, co
         return CCV3D_ERR_INVALID;
     if ((long long)d->N * frames == 0) return CCV3D_OK;
     if (out == nullptr || codes == nullptr || scales == nullptr) return CCV3D_ERR_INVALID;
-    if ((long long)d->N * frames > 65535) return CCV3D_ERR_UNSUPPORTED;
+    if ((long long)d->N * frames > CCV3D_QCACHE_MAX_FRAMES) return CCV3D_ERR_UNSUPPORTED;
     QCacheJob j = qcache_job(d);
     Buffers bufs;
     bufs.in(codes, cb);

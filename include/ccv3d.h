@@ -430,9 +430,12 @@ typedef enum {
     CCV3D_Q_E2M1 = 2  /* 4-bit float, largest 6; two per byte, the even channel low */
 } ccv3d_qformat;
 
+#define CCV3D_QCACHE_MAX_FRAMES 65535 /* N * frames that one call writes or reads */
+
 typedef struct {
-    int N, C, H, W;    /* batch entries, channels (<= 65536), spatial size */
-    int ring_slots;    /* frames the ring holds per batch entry, >= 1 */
+    int N, C, H, W;    /* batch entries, channels (<= 65536), spatial size (H * W < 2^31) */
+    int ring_slots;    /* frames the ring holds per batch entry, >= 1; N * ring_slots < 2^31,
+                          and at most 10^13 values in all */
     ccv3d_qformat format;
     ccv3d_dtype dtype; /* of the frames written and read */
 } ccv3d_qcache_desc;
@@ -445,7 +448,9 @@ CCV3D_API ccv3d_status ccv3d_qcache_sizes(const ccv3d_qcache_desc* desc, size_t*
                                           size_t* scale_bytes);
 
 /* Quantise frames first .. first + frames - 1 of x [N, T_x, H, W, C] into slots
- * (slot + i) mod ring_slots.  frames <= ring_slots; no other slot changes. */
+ * (slot + i) mod ring_slots.  frames <= ring_slots (INVALID); no other slot
+ * changes.  N * frames <= CCV3D_QCACHE_MAX_FRAMES (UNSUPPORTED), here, in a read
+ * and in ccv3d_forward_qring (the frames it reads, and those it writes). */
 CCV3D_API ccv3d_status ccv3d_qcache_write(const ccv3d_qcache_desc* desc, const void* x, int T_x,
                                           int first, int frames, int slot, void* codes,
                                           void* scales, cudaStream_t stream);
@@ -458,8 +463,9 @@ CCV3D_API ccv3d_status ccv3d_qcache_read(const ccv3d_qcache_desc* desc, const vo
 
 /* ccv3d_forward_ring with the ring held in 8 or 4 bits: reads the plan's
  * cache_len frames from head on into cache_buf ([N, cache_len, H, W, Cin], a
- * scratch that any number of modules can share; NULL allowed iff cache_len is
- * 0), runs the convolution on them, and quantises the n_w = min(K', T_x) last
+ * scratch that any number of modules can share whose calls are ordered on the
+ * GPU, as those of one stream are; calls that may overlap each need their own;
+ * NULL allowed iff cache_len is 0), runs the convolution on them, and quantises the n_w = min(K', T_x) last
  * frames of x, K' = min(cache_keep, |Z|) with the plan's cache_keep, into the
  * slots after the cached ones.  head, ring_slots, next_head and the order of
  * slots are those of ccv3d_forward_ring; out is ccv3d_forward's on the cache as
@@ -477,7 +483,8 @@ CCV3D_API ccv3d_status ccv3d_forward_qring(ccv3d_plan_t plan, const void* x,
  * current device: waits for the work queued on `stream`, then returns and
  * clears the first error their kernels recorded on the device -- CCV3D_OK,
  * CCV3D_ERR_TIMEOUT (a bounded wait of a norm or a product ran out: that call's
- * outputs are not valid) or, in the bounds-checked build, CCV3D_ERR_BOUNDS.  Allocates nothing.  Errors: CUDA. */
+ * outputs are not valid) or, in the bounds-checked build, CCV3D_ERR_BOUNDS.
+ * Allocates nothing.  Errors: CUDA. */
 CCV3D_API ccv3d_status ccv3d_block_get_status(cudaStream_t stream);
 
 /* ------------------------------------------------------------------------

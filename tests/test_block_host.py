@@ -301,3 +301,32 @@ def test_forward_qring_checks_sizes():
                                               (1, 1), (1, 1, 1), stream=0)
     finally:
         ccv3d.ccv3d_destroy(plan)
+
+
+@pytest.mark.parametrize("over", [
+    dict(H=1 << 15, W=1 << 16), dict(N=1 << 16, ring_slots=1 << 15),
+    dict(N=1 << 14, ring_slots=1 << 14, H=64, W=64, C=64)])
+def test_qcache_stated_limits(over):
+    with pytest.raises(ccv3d.CCV3DError) as e:
+        ccv3d.ccv3d_qcache_sizes(qdesc(**over))
+    assert e.value.status == CCV3D_ERR_UNSUPPORTED
+
+
+def test_qcache_frames_of_a_call():
+    """N * frames past what one call moves, for the write, the read and both in
+    ccv3d_forward_qring; the last that it moves gets past that check."""
+    N = 1 << 14
+    d = qdesc(N=N, H=1, W=1, C=8, ring_slots=5)
+    far = [(i + 1) << 32 for i in range(7)]
+    for frames, status in ((4, CCV3D_ERR_UNSUPPORTED), (3, CCV3D_ERR_ALIAS)):
+        assert ccv3d.ccv3d_qcache_write(d, far[0], 5, 0, frames, 0, far[1], far[1], stream=0,
+                                        check=False) == status
+        assert ccv3d.ccv3d_qcache_read(d, far[1], far[2], 0, frames, far[1], stream=0,
+                                       check=False) == status
+    for T_x, cache_len in ((4, 0), (1, 4)):
+        plan = ccv3d.Plan(ccv3d.make_desc(N=N, Cin=8, Cout=8, H=1, W=1, T_x=T_x,
+                                          cache_len=cache_len, cache_keep=4))
+        rc, _ = ccv3d.ccv3d_forward_qring(plan.handle, far[0], d, far[1], far[2], 0, far[3], far[4],
+                                          far[5], far[6], (1, 1), (1, 1), (1, 1, 1), stream=0,
+                                          check=False)
+        assert rc == CCV3D_ERR_UNSUPPORTED
