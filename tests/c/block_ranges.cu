@@ -16,7 +16,7 @@ int status_of(F&& f) {
     int zero = 0, status = 0;
     if (cudaMemcpyToSymbol(g_block_status, &zero, sizeof(int)) != cudaSuccess) return -1;
     f();
-    if (cudaDeviceSynchronize() != cudaSuccess ||
+    if (cudaGetLastError() != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess ||
         cudaMemcpyFromSymbol(&status, g_block_status, sizeof(int)) != cudaSuccess)
         return -1;
     return status;

@@ -34,7 +34,7 @@ int with_copy_left_out(int which, int* issued, F&& f) {
         cudaMemcpyToSymbol(g_block_status, &zero, sizeof(int)) != cudaSuccess)
         return -1;
     f();
-    if (cudaDeviceSynchronize() != cudaSuccess ||
+    if (cudaGetLastError() != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess ||
         cudaMemcpyFromSymbol(issued, g_issued, sizeof(int)) != cudaSuccess ||
         cudaMemcpyFromSymbol(&status, g_block_status, sizeof(int)) != cudaSuccess)
         return -1;

@@ -23,8 +23,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 def ranges(tmp_path_factory):
     so = str(tmp_path_factory.mktemp("ranges") / "block_ranges.so")
     subprocess.check_call([build._nvcc(), *build.ARCH, "-DCCV3D_CHECKED", "-O1", "-std=c++17",
-                           "-shared", "-Xcompiler", "-fPIC", "-I", os.path.join(build.ROOT, "include"),
-                           "-I", build.CSRC, os.path.join(HERE, "c", "block_ranges.cu"), "-o", so])
+                           "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+                           "-I", os.path.join(build.ROOT, "include"), "-I", build.CSRC,
+                           os.path.join(HERE, "c", "block_ranges.cu"), "-o", so])
     lib = ctypes.CDLL(so)
     p, ll, i = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int
     lib.cache_write.argtypes = lib.cache_read.argtypes = [p] * 3 + [i] * 6

@@ -24,7 +24,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 def waits(tmp_path_factory):
     so = str(tmp_path_factory.mktemp("waits") / "block_waits.so")
     subprocess.check_call([build._nvcc(), *build.ARCH, "-O3", "-std=c++17", "-shared", "-Xcompiler",
-                           "-fPIC", "-I", os.path.join(build.ROOT, "include"), "-I", build.CSRC,
+                           "-fPIC,-fvisibility=hidden", "-I", os.path.join(build.ROOT, "include"),
+                           "-I", build.CSRC,
                            os.path.join(HERE, "c", "block_waits.cu"), "-o", so])
     lib = ctypes.CDLL(so)
     p, ll, i, ip = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.POINTER(ctypes.c_int)
