@@ -433,8 +433,14 @@ ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb
 template <typename T, int MR, int CPW>
 void run_rows(const T* x, const T* w, int K, const PwOut& o, cudaStream_t st) {
     const unsigned grid = (unsigned)up(o.N, CPW);
-    if (K % 8 == 0) pw_rows_kernel<T, MR, CPW, true><<<grid, 256, 0, st>>>(x, w, K, o);
-    else pw_rows_kernel<T, MR, CPW, false><<<grid, 256, 0, st>>>(x, w, K, o);
+    // (bf16 rows of multiples of 8 are pw_rows_mma_kernel's)
+    if constexpr (sizeof(T) == 4) {
+        if (K % 8 == 0) {
+            pw_rows_kernel<T, MR, CPW, true><<<grid, 256, 0, st>>>(x, w, K, o);
+            return;
+        }
+    }
+    pw_rows_kernel<T, MR, CPW, false><<<grid, 256, 0, st>>>(x, w, K, o);
 }
 
 template <typename T>

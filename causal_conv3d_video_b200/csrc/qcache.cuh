@@ -61,9 +61,9 @@ __device__ __forceinline__ int scale_byte(float a, int fmt) {
 // written and read back: 182 -> 166 us).
 __device__ __forceinline__ uint2 encode8(const f2 (&x)[4], int c, int fmt) {
     if (c >= 255) return make_uint2(0u, 0u);
-    // 2^(127 - c) has exponent field 254 - c (1 <= c <= 254; c = 254: 2^-127, subnormal)
-    const f2 k = f2_all(c == 254 ? __uint_as_float(0x400000u)
-                                 : __uint_as_float((uint32_t)(254 - c) << 23));
+    // 2^(127 - c) has exponent field 254 - c; scale_byte gives 1 to 253 (the largest
+    // finite exponent field is 254, every format's top exponent at least 2)
+    const f2 k = f2_all(__uint_as_float((uint32_t)(254 - c) << 23));
     uint32_t w[2] = {0u, 0u};
     if (fmt == kQInt8) {
         const f2 magic = f2_all(12582912.0f);
