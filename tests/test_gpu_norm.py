@@ -388,3 +388,26 @@ def status_is_clean():
     an address outside its buffer) in the library's status word."""
     yield
     assert ccv3d.ccv3d_block_get_status() == ccv3d.CCV3D_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,C", SHAPES + TILED)
+def test_backward_layer_norms_without_biases(rows, C, dtype):
+    """The form of layer norms alone: two column sums, and the rows' means."""
+    _check_backward(_case(rows, C, dtype, residual=True, gates=1, pre="layer", post="layer",
+                          actk="gelu", seed=3))
+    _check_backward(_case(rows, C, dtype, residual=True, pre="layer", post="rms", actk="silu",
+                          seed=4))
+    _check_backward(_case(rows, C, dtype, pre="layer", weights=False, seed=5), dh_out=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,C", [(36, 776), (60, 1000), (24, 1025), (48, 2048), (12, 4104),
+                                    (24, 5001), (12, 8185), (12, 8192), (3600, 1024)])
+def test_wide_rows_with_several_gates(rows, C, dtype):
+    for gates, pre, post, bias in [(3, "rms", "rms", False), (12, "layer", "layer", False),
+                                   (2, "layer", "rms", True), (rows, "none", "layer", True)]:
+        s = _case(rows, C, dtype, residual=True, gates=gates, pre=pre, post=post, bias=bias,
+                  actk="silu" if pre != "none" else "none", seed=gates)
+        _check_forward(s)
+        _check_backward(s)
