@@ -9,8 +9,9 @@ import oracle
 from block_util import d, norm
 from causal_conv3d_video_b200 import ccv3d
 from causal_conv3d_video_b200.workloads import Conv
-from parity_util import assert_close, oracle_params
+from parity_util import assert_close, oracle_params, plan_env
 from test_gpu_qcache import quantise
+from test_gpu_ring import RING_SIGS
 
 pytestmark = pytest.mark.gpu
 EPS = 1e-6
@@ -246,6 +247,233 @@ torch.cuda.synchronize()
 got = [t.clone() for t in out]
 call()
 torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, out))
+assert ccv3d.ccv3d_block_get_status() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code, which], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def _qring_against_dense(conv, env, fmt, chunks, extra=0, check_oracle=True):
+    """forward_qring chunk by chunk against the same plan's forward on the frames
+    that the ring gives back: the same bits, whatever kernel convolves."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    dt = torch.bfloat16 if conv.dtype == "bf16" else torch.float32
+    rnd = lambda *s, std=1.0: (torch.randn(s, device="cuda", generator=g) * std).to(dt)
+    w = rnd(conv.Cout, conv.kt, conv.kh, conv.kw, conv.Cin,
+            std=(conv.kt * conv.kh * conv.kw * conv.Cin) ** -0.5)
+    b = rnd(conv.Cout, std=0.1) if conv.has_bias else None
+    slots = conv.cache_keep + min(conv.cache_keep, conv.T_x) + extra
+    desc = ccv3d.make_qcache_desc(N=conv.N, H=conv.H, W=conv.W, C=conv.Cin, ring_slots=slots,
+                                  format=fmt, dtype=conv.dtype)
+    codes, scales = ccv3d.alloc_qcache(desc)
+    head, length = slots - 1, 0
+    for _ in range(chunks):
+        c = conv.replace(cache_len=length)
+        with plan_env(env):
+            plan = ccv3d.Plan(ccv3d.desc_for(c))
+        x = rnd(c.N, c.T_x, c.H, c.W, c.Cin)
+        cache = torch.empty(c.N, length, c.H, c.W, c.Cin, dtype=dt, device="cuda") if length else None
+        if length:
+            ccv3d.ccv3d_qcache_read(desc, codes, scales, head, length, cache)
+        want, nc = plan.alloc_outputs("cuda")
+        plan.forward(x, cache, w, b, want, nc)
+        out, _ = plan.alloc_outputs("cuda")
+        out.fill_(float("nan"))
+        buf = torch.full_like(cache, float("nan")) if length else None
+        before = codes.clone()
+        new_head = plan.forward_qring(x, desc, codes, scales, head, buf, w, b, out)
+        torch.cuda.synchronize()
+        assert plan.status() == ccv3d.CCV3D_OK
+        assert torch.equal(out, want), (c.name, plan.kernel, length)
+        assert buf is None or torch.equal(buf, cache)
+        writes, keep = plan.ring_writes(), plan.sizes["new_cache_frames"]
+        assert new_head == (head + length + writes - keep) % slots
+        fresh = torch.zeros_like(codes)
+        ccv3d.ccv3d_qcache_write(desc, x, c.T_x, c.T_x - writes, writes, (head + length) % slots,
+                                 fresh, scales.clone())
+        at = [(head + length + i) % slots for i in range(writes)]
+        shape = (c.N, slots, -1)
+        for s in range(slots):
+            ref = fresh if s in at else before
+            assert torch.equal(codes.view(shape)[:, s], ref.view(shape)[:, s]), (c.name, s)
+        if check_oracle:
+            ref, _ = oracle.forward(oracle_params(c), _np(x), _np(cache) if length else None, _np(w),
+                                    _np(b) if b is not None else None)
+            assert_close(_np(out), ref, c.dtype, c.name)
+        head, length = new_head, keep
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e2m1"])
+@pytest.mark.parametrize("conv,env", RING_SIGS, ids=lambda v: getattr(v, "name", None) or "env")
+def test_forward_qring_every_kernel(conv, env, fmt):
+    _qring_against_dense(conv, env, fmt, 4, extra=1)
+
+
+@pytest.mark.parametrize("conv", [
+    Conv("q384_90x160", 384, 384, 90, 160, T_x=1, cache_len=0),
+    Conv("q192_360x640_t2", 192, 192, 360, 640, T_x=2, cache_len=0),
+    Conv("q96_720x1280_t4", 96, 96, 720, 1280, T_x=4, cache_len=0),
+    Conv("q96to3_720x1280_t4", 96, 3, 720, 1280, T_x=4, cache_len=0),
+], ids=lambda c: c.name)
+def test_forward_qring_decoder_sizes(conv):
+    """The kernels that the planner picks at the decoder's own sizes."""
+    _qring_against_dense(conv, {}, "e4m3", 3, check_oracle=False)
+
+
+def _poison(tensors):
+    for t in tensors:
+        t.fill_(255 if t.dtype == torch.uint8 else float("nan"))
+
+
+def test_two_streams_overlapping_from_poison():
+    """Two jobs of all the operators, each captured three times in a row, replayed
+    at once on two streams from poisoned outputs, workspaces and rings: after each
+    round the bits of the jobs run one after the other, and the replays did
+    overlap."""
+    def job(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda *s: torch.randn(s, device="cuda", generator=g).bfloat16()
+        M, C, K = 24000, 96, 192
+        x, w, res, dout = rnd(M, K), rnd(C, K), rnd(M, C), rnd(M, C)
+        nw, gate = rnd(C), rnd(3, C)
+        nd = ccv3d.make_norm_desc(rows=M, C=C, post="rms", act="silu", gate_rows=M // 3)
+        pd = ccv3d.make_pointwise_desc(pixels=M, Cin=K, Cout=C, act="silu")
+        few = ccv3d.make_pointwise_desc(pixels=5, Cin=K, Cout=C)
+        qd = ccv3d.make_qcache_desc(N=1, H=120, W=200, C=C, ring_slots=2, format="e4m3")
+        ws = [ccv3d.alloc_workspace(n) for n in (ccv3d.ccv3d_norm_workspace(nd),
+                                                 *ccv3d.ccv3d_pointwise_workspace(pd))]
+        codes, scales = ccv3d.alloc_qcache(qd)
+        out, pre, h, y, dh, db, dg, dw2, back = (torch.empty_like(t) for t in (
+            res, res, res, res, res, res, gate, nw, res))
+        dx, dw, dbias = torch.empty_like(x), torch.empty_like(w), torch.empty_like(nw)
+        rows = torch.empty(5, C, device="cuda").bfloat16()
+        written = [out, pre, h, y, back, dh, db, dg, dw2, dx, dw, dbias, rows]
+
+        def run():
+            ccv3d.ccv3d_pointwise_forward(pd, x, w, nw, res, out, pre, ws[1])
+            ccv3d.ccv3d_norm_forward(nd, res, out, gate, nw, None, nw, None, h, y)
+            ccv3d.ccv3d_qcache_write(qd, y, 1, 0, 1, 1, codes, scales)
+            ccv3d.ccv3d_qcache_read(qd, codes, scales, 1, 1, back)
+            ccv3d.ccv3d_norm_backward(nd, h, out, gate, nw, None, nw, None, dout, res, dh, db, dg,
+                                      dw2, None, None, None, ws[0])
+            ccv3d.ccv3d_pointwise_backward(pd, x, w, pre, db, dx, dw, dbias, ws[2])
+            ccv3d.ccv3d_pointwise_forward(few, dx[:5], w, None, None, rows, None, None)
+
+        return run, written, [t for t in (*ws, codes, scales) if t is not None]
+
+    jobs = [job(1), job(2)]
+    want = []
+    for run, written, scratch in jobs:
+        _poison(written + scratch)
+        run()
+        torch.cuda.synchronize()
+        assert all(t.isfinite().all() for t in written)
+        want.append([t.clone() for t in written])
+    graphs, streams = [], [torch.cuda.Stream() for _ in jobs]
+    for (run, _, _), st in zip(jobs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(3):
+                run()
+        graphs.append(g)
+    overlapped = False
+    for _ in range(10):
+        for _, written, scratch in jobs:
+            _poison(written + scratch)
+        torch.cuda.synchronize()
+        ev = [[torch.cuda.Event(enable_timing=True) for _ in range(2)] for _ in jobs]
+        for g, st, (a, b) in zip(graphs, streams, ev):
+            with torch.cuda.stream(st):
+                a.record()
+                g.replay()
+                b.record()
+        torch.cuda.synchronize()
+        for (_, written, _), ref in zip(jobs, want):
+            assert all(torch.equal(t, r) for t, r in zip(written, ref))
+        # the second began before the first ended, and ended after it began
+        overlapped |= ev[1][0].elapsed_time(ev[0][1]) > 0 and ev[0][0].elapsed_time(ev[1][1]) > 0
+    assert overlapped
+
+
+@pytest.mark.parametrize("which", ["norm", "pointwise", "few", "qcache"])
+def test_first_call_inside_a_capture_computes(which):
+    """As above from poisoned outputs, the replay and an eager call each against
+    the definition in 64 bits."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys, torch
+sys.path[:0] = ["tests"]
+from block_util import HALF, ROW, act, close, d, norm
+from causal_conv3d_video_b200 import ccv3d
+gen = torch.Generator(device="cuda").manual_seed(1)
+bf = lambda *s: torch.randn(s, device="cuda", generator=gen).bfloat16()
+half = HALF["bf16"]
+acc = lambda k: (k + 16) * 2.0 ** -23
+if sys.argv[1] == "norm":
+    h, w = bf(1000, 96), bf(96)
+    out = [torch.empty_like(h), torch.empty_like(h), torch.empty_like(w)]
+    nd = ccv3d.make_norm_desc(rows=1000, C=96)
+    ws = ccv3d.alloc_workspace(ccv3d.ccv3d_norm_workspace(nd))
+    def call():
+        ccv3d.ccv3d_norm_forward(nd, h, None, None, None, None, w, None, None, out[0])
+        ccv3d.ccv3d_norm_backward(nd, h, None, None, None, None, w, None, h, None, out[1], None,
+                                  None, None, None, out[2], None, ws)
+    def check():
+        y, n, rstd, mag = norm(d(h), "rms", d(w), None, 1e-6)
+        close(out[0], y, half * y.abs() + ROW["bf16"] * mag, "y")
+        dn = d(h) * d(w)
+        dh = rstd * (dn - n * (dn * n).mean(1, keepdim=True))
+        m = rstd * (dn.abs() + n.abs() * (dn * n).abs().mean(1, keepdim=True))
+        close(out[1], dh, half * dh.abs() + 4 * ROW["bf16"] * m, "dh")
+        t = d(h) * n
+        close(out[2], t.sum(0), half * t.sum(0).abs() + 4 * ROW["bf16"] * t.abs().sum(0), "dw")
+elif sys.argv[1] in ("pointwise", "few"):
+    M = 1000 if sys.argv[1] == "pointwise" else 5
+    x, w, g = bf(M, 192), bf(96, 192), bf(M, 96)
+    out = [bf(M, 96), torch.empty_like(x), torch.empty_like(w)]
+    pd = ccv3d.make_pointwise_desc(pixels=M, Cin=192, Cout=96)
+    ws = [ccv3d.alloc_workspace(n) for n in ccv3d.ccv3d_pointwise_workspace(pd)]
+    def call():
+        ccv3d.ccv3d_pointwise_forward(pd, x, w, None, None, out[0], None, ws[0])
+        ccv3d.ccv3d_pointwise_backward(pd, x, w, None, g, out[1], out[2], None, ws[1])
+    def check():
+        for got, a, b, k in ((out[0], d(x), d(w).t(), 192), (out[1], d(g), d(w), 96),
+                             (out[2], d(g).t(), d(x), M)):
+            want = a @ b
+            close(got, want, half * want.abs() + acc(k) * (a.abs() @ b.abs()), "product")
+else:
+    # integers with a 127 in each group of 32: scale 1, read back as they are
+    x = torch.randint(-127, 128, (1, 1, 8, 8, 96), device="cuda", generator=gen).bfloat16()
+    x[..., ::32] = 127
+    qd = ccv3d.make_qcache_desc(N=1, H=8, W=8, C=96, ring_slots=2)
+    out = [torch.empty_like(x), *ccv3d.alloc_qcache(qd)]
+    def call():
+        ccv3d.ccv3d_qcache_write(qd, x, 1, 0, 1, 1, out[1], out[2])
+        ccv3d.ccv3d_qcache_read(qd, out[1], out[2], 1, 1, out[0])
+    def check():
+        assert torch.equal(out[0], x)
+        assert (out[2].view(2, -1)[1] == 127).all() and (out[2].view(2, -1)[0] == 255).all()
+def poison():
+    for t in out:
+        t.fill_(255 if t.dtype == torch.uint8 else float("nan"))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    call()
+poison()
+graph.replay()
+torch.cuda.synchronize()
+check()
+got = [t.clone() for t in out]
+poison()
+call()
+torch.cuda.synchronize()
+check()
 assert all(torch.equal(a, b) for a, b in zip(got, out))
 assert ccv3d.ccv3d_block_get_status() == 0
 """
