@@ -84,9 +84,7 @@ size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 // (blocks on one SM share its time), in FMAs at about 83 a cycle and SM for the
 // largest tile; the others' count 1.5 times (half the FMAs per shared-memory
 // read).  Splits are of at least 8 steps of 16; joining them is a launch and two
-// trips of the partials.  A sum of more than 4096 terms (dw over many pixels)
-// is split for its accuracy too, as far as 256 MB of partials allow: one chain
-// of 12318 fp32 FMAs is 1.1e-6 off (2-norm), chains of 4096 half of that.
+// trips of the partials.
 struct SimtShape {
     int tm, tn, splits;
     long long tiles, k_per_split;
@@ -95,13 +93,12 @@ SimtShape simt_shape(long long M, long long N, long long K) {
     constexpr int kTiles[4][2] = {{128, 128}, {64, 64}, {128, 32}, {32, 128}};
     SimtShape best = {};
     double cost = 1e300;
-    const long long fit = std::max<long long>(1, std::min<long long>((256LL << 20) / (M * N * 4), 16384));
-    const long long least = std::min(up(K, 4096), fit);
     for (const auto& t : kTiles) {
         const long long tiles = up(M, t[0]) * up(N, t[1]);
-        for (const int more : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 64, 128}) {
-            const long long want = least * more;
-            if (more > 1 && (want > up(K, 128) || want > 512 || tiles * want > 8 * kSms)) break;
+        // (the last two: a block an SM, and two)
+        const int fill = (int)std::max<long long>(1, kSms / tiles);
+        for (const int want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 256, 512, fill, 2 * fill}) {
+            if (want > 1 && (want > up(K, 128) || tiles * want > 8 * kSms)) continue;
             const long long per = up(up(K, want), kPwK) * kPwK;
             const int splits = (int)std::max<long long>(1, up(K, per));
             double c = std::ceil((double)tiles * splits / kSms) * (double)t[0] * t[1] * (per + 32) *
@@ -419,10 +416,23 @@ ccv3d_status run_simt(const void* A, const void* B, long long lda, long long ldb
     p.o.partial = p.splits > 1 ? partial : nullptr;
     if (s.tiles > 0x7fffffffLL) return CCV3D_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)s.tiles, 1, p.splits);
-    if (s.tm == 32) pw_simt_kernel<float, AK, BK, 32, 128><<<grid, 256, 0, st>>>(p);
-    else if (s.tn == 128) pw_simt_kernel<float, AK, BK, 128, 128><<<grid, 256, 0, st>>>(p);
-    else if (s.tn == 64) pw_simt_kernel<float, AK, BK, 64, 64><<<grid, 256, 0, st>>>(p);
-    else pw_simt_kernel<float, AK, BK, 128, 32><<<grid, 256, 0, st>>>(p);
+    // more than one chain: room for the sums of whole ones
+    const bool chains = std::min(K, s.k_per_split) > kPwChain;
+    auto run = [&](auto tm, auto tn) {
+        if (chains) {
+            allow_smem<pw_simt_kernel<float, AK, BK, tm(), tn(), true>, tm() * tn() * 4>();
+            pw_simt_kernel<float, AK, BK, tm(), tn(), true><<<grid, 256, tm() * tn() * 4, st>>>(p);
+        } else {
+            pw_simt_kernel<float, AK, BK, tm(), tn(), false><<<grid, 256, 0, st>>>(p);
+        }
+    };
+    const std::integral_constant<int, 128> i128;
+    const std::integral_constant<int, 64> i64;
+    const std::integral_constant<int, 32> i32;
+    if (s.tm == 32) run(i32, i128);
+    else if (s.tn == 128) run(i128, i128);
+    else if (s.tn == 64) run(i64, i64);
+    else run(i128, i32);
     if (p.splits > 1) {
         const long long blocks = std::min<long long>(up(M * (p.ldp / 4), 256), kSms * 16LL);
         pw_join_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(partial, p.splits, p.ldp, o);

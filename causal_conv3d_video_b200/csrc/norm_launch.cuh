@@ -65,8 +65,8 @@ inline TileLaunch tile_launch(const RowShape& r, int C, int e, long long rows, i
     return l;
 }
 
-// Dynamic shared memory of up to 200 KB for a kernel, once per device.
-template <auto* K>
+// Dynamic shared memory of up to kBytes for a kernel, once per device.
+template <auto* K, int kBytes = 200 * 1024>
 void allow_smem() {
     constexpr int kDevices = 64;
     static std::atomic<bool> done[kDevices];
@@ -76,7 +76,7 @@ void allow_smem() {
         return;
     }
     if (done[dev].load(std::memory_order_acquire)) return;
-    cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     cudaGetLastError();
     done[dev].store(true, std::memory_order_release);
 }

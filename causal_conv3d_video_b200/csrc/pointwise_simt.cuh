@@ -44,6 +44,11 @@ __device__ __forceinline__ void pw_store(const PwOut& o, long long m, int n, flo
 }
 
 constexpr int kPwK = 16, kPwPad = 4;
+// Terms of one chain of FMAs.  Roundings add up along a chain like a random walk
+// of steps up to 2^-24 of the running sum, so its error grows as the root of its
+// length (3515 terms: 1.1e-6 off in the 2-norm).  Chains of 1024 stay near 6e-7,
+// and their sums, added up apart, near that for a hundred thousand terms.
+constexpr int kPwChain = 1024;
 
 // A thread's part of an operand tile of R rows x 16 k: with 16-byte rows kV
 // values along the contiguous direction, otherwise kV single ones, 16 rows
@@ -119,8 +124,12 @@ struct PwFetch {
 // through two shared-memory buffers; the next step's operands wait in
 // registers.  A thread has 4 rows by 4 columns of each SM/GM x SN/GN part.  The
 // largest has the best ratio of FMAs to shared-memory reads, the others are for
-// products whose edges or few tiles would idle much of it.
-template <typename T, bool AK, bool BK, int SM, int SN>
+// products whose edges or few tiles would idle much of it.  kChains: a block sums
+// more than kPwChain terms; the sums are kept in dynamic shared memory, SM * SN
+// floats, a thread's own places, to which the accumulators are added after every
+// chain.  (A form of its own: with the test in it the loop of the others takes up
+// to 6 % longer.)
+template <typename T, bool AK, bool BK, int SM, int SN, bool kChains>
 __global__ void __launch_bounds__(256, SM * SN == 128 * 128 ? 2 : 4) pw_simt_kernel(
     const __grid_constant__ PwSimt p) {
     constexpr int kTx = SN == 32 ? 8 : (SM == 32 ? 32 : 16), kTy = 256 / kTx;  // threads across, down
@@ -129,6 +138,7 @@ __global__ void __launch_bounds__(256, SM * SN == 128 * 128 ? 2 : 4) pw_simt_ker
     typedef float SlabA[2][kPwK][SM + kPwPad];
     typedef float SlabB[2][kPwK][SN + kPwPad];
     __shared__ __align__(16) float smem[kA + kB];
+    extern __shared__ __align__(16) float pw_sums[];
     SlabA& sa = *reinterpret_cast<SlabA*>(smem);
     SlabB& sb = *reinterpret_cast<SlabB*>(smem + kA);
     constexpr int kGm = kTy * 4, kGn = kTx * 4;  // rows and columns of a part
@@ -154,6 +164,27 @@ __global__ void __launch_bounds__(256, SM * SN == 128 * 128 ? 2 : 4) pw_simt_ker
     fa(va, left);
     fb(vb, left);
     int cur = 0;
+    // (16 bytes of each thread side by side)
+    [[maybe_unused]] ulonglong2* sums = reinterpret_cast<ulonglong2*>(pw_sums) + tid;
+    [[maybe_unused]] auto chain_ends = [&](bool add, bool store) {
+#pragma unroll
+        for (int i = 0; i < kHm * 4; ++i)
+#pragma unroll
+            for (int j = 0; j < kHn; ++j) {
+                ulonglong2& at = sums[(i * kHn + j) * 256];
+                f2 &a = acc[i][2 * j], &b = acc[i][2 * j + 1];
+                if (add) {
+                    const ulonglong2 t = at;
+                    a = f2_add(a, t.x);
+                    b = f2_add(b, t.y);
+                }
+                if (store) {
+                    at = make_ulonglong2(a, b);
+                    a = b = f2_all(0.0f);
+                }
+            }
+    };
+    [[maybe_unused]] int whole = left;  // what was left at the end of the last whole chain
     for (; left > 0; left -= kPwK, cur ^= 1) {
         fa.put(sa[cur], va, tid);
         fb.put(sb[cur], vb, tid);
@@ -187,7 +218,15 @@ __global__ void __launch_bounds__(256, SM * SN == 128 * 128 ? 2 : 4) pw_simt_ker
         }
         // (one barrier a step: the next step writes the other buffer, whose
         // readers passed this step's barrier)
+        if constexpr (kChains) {
+            if (whole - left == kPwChain - kPwK && left > kPwK) {
+                chain_ends(whole != (int)(ke - kb), true);
+                whole = left - kPwK;
+            }
+        }
     }
+    if constexpr (kChains)
+        if (whole != (int)(ke - kb)) chain_ends(true, false);
     // Epilogue, a row of parts at a time through shared memory: the loop over
     // its values is then short (unrolled over the accumulators it outgrew the
     // instruction cache) and runs along the rows of out.  Four values' residuals

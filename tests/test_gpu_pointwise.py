@@ -191,6 +191,35 @@ def test_fp32_long_sums_keep_their_accuracy():
         assert (d(got[k]) - want).norm() <= 1.0e-6 * want.norm(), k
 
 
+@pytest.mark.parametrize("M,K,N,which", [
+    (17_571, 200, 300, "dw"), (17_571, 988, 864, "dw"), (90_000, 40, 72, "dw"),
+    (300, 4096, 520, "out"), (40_000, 2048, 24, "out"), (300, 77, 4099, "dx"), (520, 1030, 130, "out")])
+def test_fp32_chains(M, K, N, which):
+    """Sums of many terms in fp32 are taken in chains of 1024.  With terms of random
+    signs the running sum after i of n terms is as the root of i, a rounding of it
+    2^-24 / sqrt(3) relative, so a chain is 2^-24 sqrt(n / 6) of its sum off in the
+    2-norm, 7.8e-7 for 1024; the chains' sums, at most 90 in a row, add 2^-24
+    sqrt(90 / 6) = 2.3e-7, the result's rounding 3.4e-8: 8.2e-7 in all."""
+    s = _case(M, K, N, "fp32", bias=False)
+    if which == "out":
+        got, want = _forward(s)[0], d(s["x"]) @ d(s["w"]).t()
+    else:
+        _, dout, g = _backward(s, ("x",) if which == "dx" else ("w",))
+        got = g[which]
+        want = d(dout) @ d(s["w"]) if which == "dx" else d(dout).t() @ d(s["x"])
+    assert (d(got) - want).norm() <= 8.2e-7 * want.norm()
+
+
+@pytest.mark.parametrize("terms", [1008, 1024, 1025, 1040, 1041, 2048, 2049, 2064, 3090])
+def test_fp32_around_whole_chains(terms):
+    """Sums that end at, just before and just after a whole chain, on each tile."""
+    for M, N in ((1500, 1400), (700, 70), (9000, 20), (20, 9000)):
+        _check_forward(_case(M, terms, N, "fp32", actk="silu", residual=True), pre=True)
+    for K, N in ((700, 900), (24, 40)):
+        _check_backward(_case(terms, K, N, "fp32"), ("w", "bias"))
+    _check_backward(_case(1300, 1400, terms, "fp32"), ("x",))
+
+
 def test_gradients_against_differences():
     """fp32: central differences of the 64-bit definition along random directions."""
     s = _case(40, 24, 36, "fp32", actk="gelu", bias=True)
