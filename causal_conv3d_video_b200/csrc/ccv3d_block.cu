@@ -143,12 +143,14 @@ struct TcShape {
     size_t smem, ws;
 };
 
-// Tile width and splits by the cost of the slowest pair, in SM cycles: a
-// 64-deep step of an M = 256 pair MMA of N = BN takes max(500, 2.64 BN) (four
-// instructions; measured on this GPU: about 3100 MAC a cycle and SM, and no
-// less than 125 cycles an instruction), a tile's epilogue about 12 BN beside
-// the next tile's steps, a split reduction's partials two trips at 3500
-// bytes a cycle and a launch of 4000.
+// Tile width and splits by the cost of the slowest pair, in SM cycles: a 64-deep
+// step of a 256 x BN tile takes about max(500, 2.64 BN), a tile's epilogue about
+// 12 BN beside the next tile's steps, a split reduction's partials two trips at
+// 3500 bytes a cycle and a launch of 4000.  Measured steps, one tile on each of
+// the 74 pairs, operands in L2: BN 32 438 cycles, 64 491, 96 498, 128 505, 160
+// 531, 192 533, 224 574, 256 658.  (A tile alone on the GPU takes about 450 too,
+// so the floor is not the pairs' share of L2; at 256 wide the tensor pipe is four
+// fifths busy.)
 TcShape tc_shape(long long M, int N, long long K, bool b_mn, bool res, bool pre) {
     TcShape s = {};
     s.tiles_m = (int)up(M, kPtRows);
@@ -337,8 +339,10 @@ ccv3d_status run_tc(const void* A, int lda, const void* B, int ldb, long long M,
 }
 
 // Rows up to which the warp-level kernel takes a bf16 product whose Cin is a
-// multiple of 8 (4096 x 4096: 8 rows 10.7, 16 rows 12.0, 32 rows 23 us, against
-// 15 to 18 us on the tensor-core kernel with its reduction split).
+// multiple of 8.  Us of 16 rows on it and of 17 on the tensor-core kernel with its
+// reduction split: 384 -> 1152 3.1 and 6.0, 1024 -> 4096 4.7 and 10.0, 4096 ->
+// 1024 7.8 and 9.9, 4096 -> 4096 12.8 and 16.9, 2048 -> 8192 13.5 and 16.6, 8192
+// -> 2048 17.4 and 17.4; 32 rows on it take 23 at 4096 x 4096.
 constexpr int kMmaRows = 16;
 bool few_rows(const ccv3d_pointwise_desc* d) {
     return d->pixels <= kPwFewRows ||
