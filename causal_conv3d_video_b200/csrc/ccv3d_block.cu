@@ -148,9 +148,8 @@ struct TcShape {
 // 12 BN beside the next tile's steps, a split reduction's partials two trips at
 // 3500 bytes a cycle and a launch of 4000.  Measured steps, one tile on each of
 // the 74 pairs, operands in L2: BN 32 438 cycles, 64 491, 96 498, 128 505, 160
-// 531, 192 533, 224 574, 256 658.  (A tile alone on the GPU takes about 450 too,
-// so the floor is not the pairs' share of L2; at 256 wide the tensor pipe is four
-// fifths busy.)
+// 531, 192 533, 224 574, 256 658.  (Calls of one to four rows of tiles take about
+// 450 too, so the floor is not the pairs' share of L2.)
 TcShape tc_shape(long long M, int N, long long K, bool b_mn, bool res, bool pre) {
     TcShape s = {};
     s.tiles_m = (int)up(M, kPtRows);
