@@ -515,13 +515,16 @@ def ccv3d_qcache_read(desc: ccv3d_qcache_desc, codes, scales, head: int, frames:
 
 def ccv3d_forward_qring(plan, x, desc: ccv3d_qcache_desc, codes, scales, head: int, cache_buf, w,
                         bias, out, stride, pad, dilation, stream=None, check: bool = True):
-    """ccv3d_forward_ring with the ring held in 8 or 4 bits.  Tensors
-    have to be of the sizes that the plan was made for (a plan given as a raw
-    handle is the caller's word for them).  Returns (status, next_head)."""
+    """ccv3d_forward_ring with the ring held in 8 or 4 bits.  Tensors have to be of the
+    sizes that the plan was made for; cache_buf, a scratch that modules may share,
+    may be larger.  (A plan given as a raw handle is the caller's word for them.)
+    Returns (status, next_head)."""
     dt, sizes = desc.dtype, getattr(plan, "elements", None)
     for name, t in (("x", x), ("cache_buf", cache_buf), ("w", w), ("bias", bias), ("out", out)):
-        if sizes and t is not None and type(t) is not int and t.numel() != sizes[name]:
-            raise ValueError(f"forward_qring: {name} has {t.numel()} elements, not {sizes[name]}")
+        if sizes and t is not None and type(t) is not int:
+            n = t.numel()
+            if n < sizes[name] or (n > sizes[name] and name != "cache_buf"):
+                raise ValueError(f"forward_qring: {name} has {n} elements, not {sizes[name]}")
     a, st = _operands("ccv3d_forward_qring", dt, stream, (), (
         ("x", x, None, dt), *_ring(desc, codes, scales), ("cache_buf", cache_buf, None, dt),
         ("w", w, None, dt), ("bias", bias, None, dt), ("out", out, None, dt)))

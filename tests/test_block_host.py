@@ -294,6 +294,8 @@ def test_forward_qring_checks_sizes():
     try:
         for name in good:
             for wrong in (good[name][..., :-8].contiguous(), torch.cat([good[name]] * 2)):
+                if name == "cache_buf" and wrong.numel() > good[name].numel():
+                    continue    # a scratch may be larger
                 a = dict(good, **{name: wrong})
                 with pytest.raises(ValueError, match=f"{name} has {wrong.numel()} elements"):
                     ccv3d.ccv3d_forward_qring(plan, a["x"], qdesc(), _addr(1), _addr(2), 0,

@@ -481,3 +481,26 @@ assert ccv3d.ccv3d_block_get_status() == 0
     r = subprocess.run([sys.executable, "-c", code, which], cwd=root, capture_output=True,
                        text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_forward_qring_with_a_larger_scratch():
+    """cache_buf may be larger than the call's frames: only those are written."""
+    H, W, C = 6, 10, 32
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rnd = lambda *s: torch.randn(s, device="cuda", generator=g).bfloat16()
+    x, w, b = rnd(1, 1, H, W, C), rnd(C, 3, 3, 3, C), rnd(C)
+    q = ccv3d.make_qcache_desc(N=1, H=H, W=W, C=C, ring_slots=3)
+    plan = ccv3d.Plan(ccv3d.make_desc(N=1, Cin=C, Cout=C, H=H, W=W, T_x=1, cache_len=2))
+    outs = []
+    for frames in (2, 5):
+        codes, scales = ccv3d.alloc_qcache(q)
+        ccv3d.ccv3d_qcache_write(q, rnd(1, 2, H, W, C) if not outs else held, 2, 0, 2, 0, codes, scales)
+        if not outs:
+            held = torch.empty(1, 2, H, W, C, device="cuda").bfloat16()
+            ccv3d.ccv3d_qcache_read(q, codes, scales, 0, 2, held)
+        buf = torch.full((1, frames, H, W, C), 7.0, device="cuda").bfloat16()
+        out, _ = plan.alloc_outputs("cuda")
+        assert plan.forward_qring(x, q, codes, scales, 0, buf, w, b, out) == 1
+        outs.append(out)
+        assert torch.equal(buf[:, :2], held) and (buf[:, 2:] == 7.0).all()
+    assert torch.equal(*outs)
